@@ -369,6 +369,140 @@ mole_status mole_train_backward(const int32_t* ids, int64_t T, const void* group
                                 void* cache, size_t cache_bytes, int32_t n_distinct, float* dh, float* dWr,
                                 float* dE, float* dW1, float* dW2, cudaStream_t stream);
 
+/*
+ * ---- Around the layer in a training step: embedding, block norms, optimizer ----
+ * (MoLE page, 训练阶段: the model trains end to end on the language-model loss;
+ * the embedding matrix is the model's input table and the routed experts'
+ * input.  The page gives no formulas for the parts around a layer; the forms
+ * below are this library's reading.)  All of them run on the device that is
+ * current, enqueue kernels only (no synchronisation, no allocation: a call can
+ * be captured in a CUDA graph), and give the same bits on every run.
+ *
+ * mole_embed_forward: out[t, :] = scale * E[ids[t], :], the product in fp32,
+ *   rounded once to dt_out.
+ *     ids : [T] int32 in [0, V)   E : [V, D] dt_E   out : [T, D] dt_out
+ *   A token with an id outside [0, V) gets a NaN row and sets the device error
+ *   word (MOLE_ERR_INDEX from mole_check).
+ *
+ * mole_embed_backward: dE[v, :] += scale * sum over the tokens t with
+ *   ids[t] == v of dout[t, :].  Sums in fp32 over the tokens in ascending
+ *   order (in partial sums over fixed runs of the sorted tokens), one addition
+ *   to dE per row; rows of ids that the batch does not hold are not touched.
+ *   Ids outside [0, V) contribute nothing and set the device error word.
+ *     dout : [T, D] dt   dE : [V, D] fp32 (added to)
+ *     workspace : device, 16-byte aligned, at least
+ *       mole_embed_backward_workspace(T, D) bytes; contents unspecified on
+ *       return; calls that share one must not overlap on the GPU.
+ *
+ * Both take any D up to 2^20 and T up to 2^31 - 1 (T == 0 is a no-op), and
+ * pointers aligned to their element; 16-byte aligned pointers with D a
+ * multiple of 8 take the vector kernels.
+ */
+mole_status mole_embed_forward(const int32_t* ids, int64_t T, const void* E, int64_t V, int64_t D, float scale,
+                               mole_dtype dt_E, void* out, mole_dtype dt_out, cudaStream_t stream);
+size_t mole_embed_backward_workspace(int64_t T, int64_t D);
+mole_status mole_embed_backward(const int32_t* ids, int64_t T, const void* dout, mole_dtype dt, int64_t V, int64_t D,
+                                float scale, float* dE, void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * The norms around a block, with its gate and the residual scale.  With
+ * rms(u) = sqrt(mean_d u_d^2 + eps) per token:
+ *     y  = w_post * f / rms(f)              (post-norm; y = f where w_post is NULL)
+ *     x' = res_scale * x + gate[t] * y      (gate = 1 where gate is NULL; y = 0 where f is NULL)
+ *     h  = w_pre * x' / rms(x')             (the next block's input)
+ * so one call takes a block's output f (mole_ffn_block without its residual,
+ * mole_lookup_combine, ...) to the next stream x' and the next block's input;
+ * with f NULL it is the norm before the first block, with h NULL the end of
+ * the last one.  All arithmetic in fp32; h is computed from x' before x' is
+ * rounded to dt_x.
+ *   x : [T, D] dt_x   f : [T, D] dt_f or NULL   w_post, w_pre : [D] fp32 or NULL
+ *   gate : [T] fp32 or NULL   x_out : [T, D] dt_x or NULL (may be x)
+ *   h : [T, D] dt_h or NULL (needs w_pre; not overlapping any other tensor)
+ * At least one of x_out and h; w_post and gate need f; eps > 0.
+ *
+ * mole_block_norm_backward: from the gradients of x' and h (dx_out, dh; either
+ * may be NULL = zero, not both),
+ *     G  = dx_out + d(h)/d(x')^T dh         at x' as stored (x_out, dt_x)
+ *     dx = res_scale * G,  dgate[t] = <G, y>,  df = gate[t] * d(y)/d(f)^T G
+ *     dw_pre[d] += sum_t dh x'/rms(x'),  dw_post[d] += sum_t gate[t] G f/rms(f)
+ * dx [T, D], df [T, D] and dgate [T] (fp32) are overwritten; dw_pre and dw_post
+ * ([D] fp32) are added to.  Any output may be NULL, not all.  dh needs w_pre;
+ * x_out may be NULL where dh is; dgate, w_post and dw_post need f (dw_post
+ * needs w_post too).  dx may be dx_out and df may be dh; other overlaps are
+ * not allowed.  workspace (device, 16-byte aligned):
+ * mole_block_norm_backward_workspace(T, D) bytes, needed for dw_pre and
+ * dw_post only; calls that share one must not overlap on the GPU.
+ *
+ * Both take any D up to 8192 and T up to 2^31 - 1 (T == 0 is a no-op), and
+ * pointers aligned to their element; 16-byte aligned pointers with D a
+ * multiple of 8 take the vector kernels.
+ */
+mole_status mole_block_norm_forward(const void* x, mole_dtype dt_x, const void* f, mole_dtype dt_f,
+                                    const float* w_post, const float* gate, float res_scale, const float* w_pre,
+                                    float eps, int64_t T, int64_t D, void* x_out, void* h, mole_dtype dt_h,
+                                    cudaStream_t stream);
+size_t mole_block_norm_backward_workspace(int64_t T, int64_t D);
+mole_status mole_block_norm_backward(const void* x_out, mole_dtype dt_x, const void* f, mole_dtype dt_f,
+                                     const float* w_post, const float* gate, float res_scale, const float* w_pre,
+                                     float eps, int64_t T, int64_t D, const float* dx_out, const float* dh, float* dx,
+                                     float* df, float* dgate, float* dw_post, float* dw_pre, void* workspace,
+                                     size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * One AdamW step over a list of tensors (decoupled weight decay).  Per
+ * element, in fp32, with g = grad_scale * grad, the weight p (master where
+ * there is one, else param), and t the step number, counted from 1:
+ *     m = beta1 m + (1 - beta1) g        v = beta2 v + (1 - beta2) g^2
+ *     p = p - lr weight_decay p - lr m / (1 - beta1^t) / (sqrt(v / (1 - beta2^t)) + eps)
+ * param = p rounded to its type (and master = p).  A bf16 param without a
+ * master rounds to nearest every step, so updates below half a bf16 step of
+ * the weight are lost; with a master they add up.
+ *
+ * state8 = 0: m and v are [n] fp32.
+ * state8 = 1: m and v are [n] e4m3 codes in blocks of 128 consecutive
+ *   elements with one fp32 scale each ([ceil(n / 128)]): m = code * m_scale,
+ *   sqrt(v) = code * v_scale.  The update uses the new m and v in fp32; then
+ *   scale = max(max |.| / 448, 2^-120) and codes round to nearest even, except
+ *   that a v > 0 never gets the code 0 (its element would take a step of
+ *   lr m / eps).  All-zero codes and scales are the initial state.  A
+ *   gradient that is not finite spoils the states of its whole block.
+ *
+ * The step number and the rate come from the host struct, or, where step_dev
+ * or lr_dev is not NULL, from device memory when the kernel runs (a captured
+ * step then follows them on every replay); grad_scale_dev (NULL = 1) is a
+ * factor on every gradient, such as a clipping factor computed on the device.
+ *
+ * tensors and config are HOST structs, read before the call returns.  No
+ * memory that a call writes may overlap anything else in its list
+ * (MOLE_ERR_ARG).  Any n >= 0 and pointers aligned to their element; 16-byte
+ * aligned pointers (8-byte for codes) take the vector path.  One launch per
+ * 64 tensors.
+ */
+typedef struct {
+  void* param;         /* [n] dt_param, overwritten */
+  const void* grad;    /* [n] dt_grad */
+  float* master;       /* [n] fp32 or NULL (dt_param MOLE_F32: must be NULL) */
+  void* m;             /* [n] fp32, or e4m3 codes */
+  void* v;
+  float* m_scale;      /* [ceil(n / 128)] (state8), else NULL */
+  float* v_scale;
+  int64_t n;
+  float weight_decay;
+  int32_t dt_param, dt_grad; /* mole_dtype */
+} mole_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps;
+  int64_t step;                 /* >= 1 (ignored where step_dev is given) */
+  const int64_t* step_dev;      /* device, or NULL */
+  const float* lr_dev;          /* device, or NULL */
+  const float* grad_scale_dev;  /* device, or NULL */
+  int32_t state8;
+} mole_adamw_config;
+
+mole_status mole_adamw_step(const mole_adamw_tensor* tensors, int32_t n_tensors, const mole_adamw_config* config,
+                            cudaStream_t stream);
+
 /* The 8 NF3 levels as fp16 bit patterns (ascending; index 3 is 0.0) and the 7
  * fp32 decision midpoints.  Host-only; no device work. */
 void mole_nf3_levels(uint16_t levels_f16[8]);

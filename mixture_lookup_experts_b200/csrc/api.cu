@@ -3,19 +3,13 @@
 // stream.  No entry point allocates device memory.
 #include "common.cuh"
 
+using mole::check_device;
+
 namespace {
 
 bool valid_dtype(mole_dtype dt) { return dt == MOLE_F32 || dt == MOLE_BF16; }
 bool valid_act(mole_act a) { return a >= MOLE_ACT_GELU_ERF && a <= MOLE_ACT_IDENTITY; }
 size_t dtype_size(mole_dtype dt) { return dt == MOLE_BF16 ? 2 : 4; }
-
-mole_status check_device() {
-  int dev = 0, major = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return MOLE_ERR_NO_DEVICE;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
-    return MOLE_ERR_NO_DEVICE;
-  return major == 10 ? MOLE_OK : MOLE_ERR_NO_DEVICE;
-}
 
 // Shared checks of the two combine entry points.
 mole_status check_combine(const int32_t* ids, int64_t T, const void* h, const void* Wr, const void* table,

@@ -26,6 +26,9 @@ unsigned* error_word();
 // Number of SMs of the current device (cached per device).
 int num_sms();
 
+// MOLE_OK if the current device is an sm_100 GPU, else MOLE_ERR_NO_DEVICE.
+mole_status check_device();
+
 // Turns a launch / runtime error into a status.
 inline mole_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOLE_OK : MOLE_ERR_CUDA; }
 

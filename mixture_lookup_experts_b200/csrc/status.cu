@@ -41,6 +41,14 @@ int num_sms() {
   return g_sms[dev];
 }
 
+mole_status check_device() {
+  int dev = 0, major = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MOLE_ERR_NO_DEVICE;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
+    return MOLE_ERR_NO_DEVICE;
+  return major == 10 ? MOLE_OK : MOLE_ERR_NO_DEVICE;
+}
+
 }  // namespace mole
 
 extern "C" const char* mole_status_str(mole_status s) {

@@ -7,6 +7,7 @@ raises ``ImportError`` if it is missing -- there is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -31,6 +32,7 @@ ACT = {"gelu": 0, "gelu_erf": 0, "gelu_tanh": 1, "relu": 2, "silu": 3, "identity
 
 # Every function include/mole.h declares, with its ctypes signature.
 _P, _I64, _I32, _I, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int, ctypes.c_size_t
+_F = ctypes.c_float
 SIGNATURES = {
     "mole_status_str": ([_I], ctypes.c_char_p),
     "mole_version": ([], _I),
@@ -64,6 +66,13 @@ SIGNATURES = {
     "mole_gather_plan": ([_P, _I64, _I64, _P, _P, _P, _P], _I),
     "mole_prefetch_rows": ([_P, _I64, _P, _I32, _I64, _I64, _P], _I),
     "mole_check": ([_P, _I], _I),
+    "mole_embed_forward": ([_P, _I64, _P, _I64, _I64, _F, _I, _P, _I, _P], _I),
+    "mole_embed_backward_workspace": ([_I64, _I64], _SZ),
+    "mole_embed_backward": ([_P, _I64, _P, _I, _I64, _I64, _F, _P, _P, _SZ, _P], _I),
+    "mole_block_norm_forward": ([_P, _I, _P, _I, _P, _P, _F, _P, _F, _I64, _I64, _P, _P, _I, _P], _I),
+    "mole_block_norm_backward_workspace": ([_I64, _I64], _SZ),
+    "mole_block_norm_backward": ([_P, _I, _P, _I, _P, _P, _F, _P, _F, _I64, _I64] + [_P] * 8 + [_SZ, _P], _I),
+    "mole_adamw_step": ([_P, _I32, _P, _P], _I),
 }
 for _name, (_args, _res) in SIGNATURES.items():
     _fn = getattr(lib, _name)
@@ -464,6 +473,227 @@ def mole_prefetch_rows(ids: torch.Tensor, tables, stream=None) -> None:
     arr = (ctypes.c_void_p * len(tables))(*[t.data_ptr() for t in tables])
     _ok(lib.mole_prefetch_rows(_ptr(ids), ids.numel(), arr, len(tables), V, row_bytes, _stream(stream)),
         "mole_prefetch_rows")
+
+
+# ---- Around the layer in a training step (see mole.h) ----
+# These calls check shapes, types and devices, and run on the device that holds
+# their tensors: `stream` (default: that device's current stream) gets the
+# kernels, and what the call allocates for itself is allocated for that stream.
+
+@contextlib.contextmanager
+def _launching(stream, like: torch.Tensor):
+    """The tensors' device and `stream` made current; gives the stream handle."""
+    dev = like.device
+    with torch.cuda.device(dev):
+        if stream is None:
+            yield torch.cuda.current_stream(dev).cuda_stream
+            return
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        if stream.device != dev:
+            raise ValueError(f"stream of {stream.device}, tensors on {dev}")
+        with torch.cuda.stream(stream):
+            yield stream.cuda_stream
+
+
+def _expect(name: str, t, like: torch.Tensor, shape=None, dtypes=None) -> None:
+    """A tensor argument's device, layout, shape and type (None passes)."""
+    if t is None:
+        return
+    if not t.is_cuda or t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected a CUDA device, the same for all tensors")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if dtypes is not None and t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+
+
+_ROWS = (torch.float32, torch.bfloat16)
+_FP32 = (torch.float32,)
+_INT32 = (torch.int32,)
+
+
+def mole_embed_forward(ids: torch.Tensor, E: torch.Tensor, scale: float = 1.0, out: torch.Tensor | None = None,
+                       out_dtype=None, stream=None) -> torch.Tensor:
+    """out[t] = scale * E[ids[t]] (fp32 or bf16; out in E's type unless asked otherwise)."""
+    T = ids.numel()
+    V, D = E.shape
+    _expect("E", E, E, dtypes=_ROWS)
+    _expect("ids", ids, E, dtypes=_INT32)
+    _expect("out", out, E, (T, D), _ROWS if out_dtype is None else (out_dtype,))
+    with _launching(stream, E) as s:
+        if out is None:
+            out = torch.empty((T, D), dtype=out_dtype or E.dtype, device=E.device)
+        _ok(lib.mole_embed_forward(_ptr(ids), T, _ptr(E), V, D, scale, _dt(E), _ptr(out), _dt(out), s),
+            "mole_embed_forward")
+    return out
+
+
+def mole_embed_backward_workspace(T: int, D: int) -> int:
+    return int(lib.mole_embed_backward_workspace(T, D))
+
+
+def mole_embed_backward(ids: torch.Tensor, dout: torch.Tensor, dE: torch.Tensor, scale: float = 1.0,
+                        workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """dE[ids[t]] += scale * dout[t] (dE fp32; the same bits on every run); returns dE."""
+    T = ids.numel()
+    V, D = dE.shape
+    _expect("dE", dE, dE, dtypes=_FP32)
+    _expect("ids", ids, dE, dtypes=_INT32)
+    _expect("dout", dout, dE, (T, D), _ROWS)
+    _expect("workspace", workspace, dE)
+    with _launching(stream, dE) as s:
+        if workspace is None:
+            workspace = torch.empty(max(1, lib.mole_embed_backward_workspace(T, D)), dtype=torch.uint8,
+                                    device=dE.device)
+        _ok(lib.mole_embed_backward(_ptr(ids), T, _ptr(dout), _dt(dout), V, D, scale, _ptr(dE), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), s), "mole_embed_backward")
+    return dE
+
+
+def mole_block_norm_forward(x: torch.Tensor, f: torch.Tensor | None = None, w_post: torch.Tensor | None = None,
+                            gate: torch.Tensor | None = None, res_scale: float = 1.0,
+                            w_pre: torch.Tensor | None = None, eps: float = 1e-6, x_out: torch.Tensor | None = None,
+                            h: torch.Tensor | None = None, h_dtype=torch.bfloat16, stream=None):
+    """(x', h): x' = res_scale x + gate w_post f / rms(f), h = w_pre x' / rms(x').
+
+    x' is made where f is given or res_scale is not 1 (or x_out is passed;
+    x_out may be x), else it is x itself; h is made where w_pre is given, else
+    None.
+    """
+    T, D = x.shape
+    _expect("x", x, x, dtypes=_ROWS)
+    _expect("f", f, x, (T, D), _ROWS)
+    _expect("w_post", w_post, x, (D,), _FP32)
+    _expect("gate", gate, x, (T,), _FP32)
+    _expect("w_pre", w_pre, x, (D,), _FP32)
+    _expect("x_out", x_out, x, (T, D), (x.dtype,))
+    _expect("h", h, x, (T, D), _ROWS)
+    with _launching(stream, x) as s:
+        if x_out is None and (f is not None or res_scale != 1.0):
+            x_out = torch.empty_like(x)
+        if h is None and w_pre is not None:
+            h = torch.empty((T, D), dtype=h_dtype, device=x.device)
+        _ok(lib.mole_block_norm_forward(_ptr(x), _dt(x), _ptr(f), F32 if f is None else _dt(f), _ptr(w_post),
+                                        _ptr(gate), res_scale, _ptr(w_pre), eps, T, D, _ptr(x_out), _ptr(h),
+                                        BF16 if h is None else _dt(h), s), "mole_block_norm_forward")
+    return (x if x_out is None else x_out), h
+
+
+def mole_block_norm_backward_workspace(T: int, D: int) -> int:
+    return int(lib.mole_block_norm_backward_workspace(T, D))
+
+
+def mole_block_norm_backward(x_out: torch.Tensor, dx_out: torch.Tensor | None, dh: torch.Tensor | None,
+                             f: torch.Tensor | None = None, w_post: torch.Tensor | None = None,
+                             gate: torch.Tensor | None = None, res_scale: float = 1.0,
+                             w_pre: torch.Tensor | None = None, eps: float = 1e-6, dx: torch.Tensor | None = None,
+                             df: torch.Tensor | None = None, dgate: torch.Tensor | None = None,
+                             dw_post: torch.Tensor | None = None, dw_pre: torch.Tensor | None = None,
+                             workspace: torch.Tensor | None = None, stream=None):
+    """(dx, df, dgate) of mole_block_norm_forward from the gradients of its two
+    outputs; dw_post and dw_pre are added to where given.  df is made where f
+    is given, dgate where gate is."""
+    T, D = x_out.shape
+    _expect("x_out", x_out, x_out, dtypes=_ROWS)
+    _expect("f", f, x_out, (T, D), _ROWS)
+    for name, t in (("dx_out", dx_out), ("dh", dh), ("dx", dx), ("df", df)):
+        _expect(name, t, x_out, (T, D), _FP32)
+    for name, t in (("w_post", w_post), ("w_pre", w_pre), ("dw_post", dw_post), ("dw_pre", dw_pre)):
+        _expect(name, t, x_out, (D,), _FP32)
+    for name, t in (("gate", gate), ("dgate", dgate)):
+        _expect(name, t, x_out, (T,), _FP32)
+    _expect("workspace", workspace, x_out)
+    dev = x_out.device
+    with _launching(stream, x_out) as s:
+        if dx is None:
+            dx = torch.empty((T, D), dtype=torch.float32, device=dev)
+        if df is None and f is not None:
+            df = torch.empty((T, D), dtype=torch.float32, device=dev)
+        if dgate is None and gate is not None:
+            dgate = torch.empty((T,), dtype=torch.float32, device=dev)
+        if workspace is None and (dw_post is not None or dw_pre is not None):
+            workspace = torch.empty(max(1, lib.mole_block_norm_backward_workspace(T, D)), dtype=torch.uint8,
+                                    device=dev)
+        _ok(lib.mole_block_norm_backward(_ptr(x_out), _dt(x_out), _ptr(f), F32 if f is None else _dt(f),
+                                         _ptr(w_post), _ptr(gate), res_scale, _ptr(w_pre), eps, T, D, _ptr(dx_out),
+                                         _ptr(dh), _ptr(dx), _ptr(df), _ptr(dgate), _ptr(dw_post), _ptr(dw_pre),
+                                         _ptr(workspace),
+                                         0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                         s), "mole_block_norm_backward")
+    return dx, df, dgate
+
+
+class AdamWTensor(ctypes.Structure):
+    """mole_adamw_tensor of mole.h."""
+    _fields_ = [("param", _P), ("grad", _P), ("master", _P), ("m", _P), ("v", _P), ("m_scale", _P), ("v_scale", _P),
+                ("n", _I64), ("weight_decay", _F), ("dt_param", _I32), ("dt_grad", _I32)]
+
+
+class AdamWConfig(ctypes.Structure):
+    """mole_adamw_config of mole.h."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", _I64), ("step_dev", _P), ("lr_dev", _P), ("grad_scale_dev", _P),
+                ("state8", _I32)]
+
+
+ADAMW_BLOCK = 128  # elements per scale of an 8-bit state
+
+
+def mole_adamw_step(params, grads, ms, vs, masters=None, m_scales=None, v_scales=None, weight_decay=0.0,
+                    lr: float = 1e-3, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, step=1,
+                    lr_dev: torch.Tensor | None = None, grad_scale: torch.Tensor | None = None, stream=None) -> None:
+    """One AdamW step over the tensors of `params` (fp32 or bf16; lists of
+    equal length; see mole.h).  ms and vs are fp32, or torch.float8_e4m3fn with
+    m_scales and v_scales (fp32, one value per 128 elements).  masters: fp32
+    weights of the bf16 params (a list, entries may be None).  weight_decay: a
+    number or one per tensor.  step: the step's number from 1, or a device
+    int64 tensor that holds it; lr_dev (device fp32) replaces lr, grad_scale
+    (device fp32) multiplies every gradient."""
+    params, grads, ms, vs = list(params), list(grads), list(ms), list(vs)
+    n = len(params)
+    none = [None] * n
+    masters = none if masters is None else list(masters)
+    m_scales = none if m_scales is None else list(m_scales)
+    v_scales = none if v_scales is None else list(v_scales)
+    decay = [weight_decay] * n if isinstance(weight_decay, (int, float)) else list(weight_decay)
+    if any(len(x) != n for x in (grads, ms, vs, masters, m_scales, v_scales, decay)):
+        raise ValueError("lists of different lengths")
+    if n == 0:
+        return
+    first = params[0]
+    state8 = ms[0].dtype == torch.float8_e4m3fn
+    states = (torch.float8_e4m3fn,) if state8 else _FP32
+    arr = (AdamWTensor * n)()
+    for i, (d, p, g, w, m, v, sm, sv, wd) in enumerate(zip(arr, params, grads, masters, ms, vs, m_scales, v_scales,
+                                                           decay)):
+        shape, k = p.shape, p.numel()
+        _expect(f"params[{i}]", p, first, None, _ROWS)
+        _expect(f"grads[{i}]", g, first, shape, _ROWS)
+        _expect(f"masters[{i}]", w, first, shape, _FP32)
+        _expect(f"ms[{i}]", m, first, shape, states)
+        _expect(f"vs[{i}]", v, first, shape, states)
+        if state8:
+            blocks = ((k + ADAMW_BLOCK - 1) // ADAMW_BLOCK,)
+            _expect(f"m_scales[{i}]", sm, first, blocks, _FP32)
+            _expect(f"v_scales[{i}]", sv, first, blocks, _FP32)
+        d.param, d.grad, d.master, d.m, d.v = p.data_ptr(), g.data_ptr(), _ptr(w), m.data_ptr(), v.data_ptr()
+        d.m_scale, d.v_scale, d.n, d.weight_decay = _ptr(sm), _ptr(sv), k, wd
+        d.dt_param, d.dt_grad = _dt(p), _dt(g)
+    cfg = AdamWConfig(lr=lr, beta1=beta1, beta2=beta2, eps=eps, state8=int(state8))
+    if isinstance(step, torch.Tensor):
+        _expect("step", step, first, None, (torch.int64,))
+        cfg.step_dev = step.data_ptr()
+    else:
+        cfg.step = step
+    for name, t, field in (("lr_dev", lr_dev, "lr_dev"), ("grad_scale", grad_scale, "grad_scale_dev")):
+        if t is not None:
+            _expect(name, t, first, None, _FP32)
+            setattr(cfg, field, t.data_ptr())
+    with _launching(stream, first) as s:
+        _ok(lib.mole_adamw_step(arr, n, ctypes.addressof(cfg), s), "mole_adamw_step")
 
 
 def mole_check(stream=None, timeout_ms: int = 10000) -> int:

@@ -1,0 +1,213 @@
+"""The embedding lookup and its gradient (mole_embed_forward / _backward)
+against plain fp64 forms.  Bounds: a lookup is one product and one rounding to
+the output's type; a gradient row of c tokens is c additions, a product and the
+addition to dE (train_ops_ref)."""
+import numpy as np
+import pytest
+import torch
+
+import train_ops_ref as ref
+from helpers import dev
+from mixture_lookup_experts_b200 import inputs
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def _rand(rng, *shape, dtype=F32, std=1.0):
+    return torch.from_numpy((rng.standard_normal(shape) * std).astype(np.float32)).to(dtype).cuda()
+
+
+def _check_forward(mole, rng, T, V, D, tin, tout, ids=None, scale=3.7):
+    E = _rand(rng, V, D, dtype=tin)
+    ids = inputs.uniform_ids(rng, T, V) if ids is None else ids
+    out = mole.mole_embed_forward(dev(ids), E, scale, out_dtype=tout)
+    assert out.dtype == tout and mole.mole_check() == 0
+    want = float(np.float32(scale)) * ref.f64(E)[ids]
+    ref.assert_within(ref.f64(out), want, (ref.U + ref.HALF[tout]) * (1 + 2.0 ** -7) * np.abs(want))
+
+
+@pytest.mark.parametrize("tin", [F32, BF16])
+@pytest.mark.parametrize("tout", [F32, BF16])
+@pytest.mark.parametrize("T,V,D", [(1, 1, 1), (1, 50304, 2048), (7, 3, 8), (33, 100, 1001), (300, 50, 72),
+                                   (513, 1000, 2056), (5, 9, 4099)])
+def test_forward(mole, T, V, D, tin, tout):
+    _check_forward(mole, np.random.default_rng(T + D), T, V, D, tin, tout)
+
+
+def test_forward_ids_at_both_ends_and_bad(mole):
+    rng = np.random.default_rng(1)
+    V, D = 77, 136
+    E = _rand(rng, V, D, dtype=BF16)
+    ids = np.array([0, V - 1, -1, V, 2 ** 31 - 1, -2 ** 31, 5], np.int32)
+    out = mole.mole_embed_forward(dev(ids), E, 1.0)
+    assert mole.mole_check() == 5
+    bad = np.array([False, False, True, True, True, True, False])
+    assert torch.isnan(out[dev(bad)]).all()
+    assert torch.equal(out[dev(~bad)], E[dev(ids[~bad]).long()])
+    assert mole.mole_check() == 0
+
+
+def test_forward_from_unaligned_rows(mole):
+    # a table and an output that start inside a buffer take the scalar kernel
+    rng = np.random.default_rng(2)
+    V, D, T = 40, 64, 50
+    buf = _rand(rng, V * D + 3)
+    E = buf[3:].view(V, D)
+    out_buf = torch.full((T * D + 1,), 7.0, dtype=BF16, device="cuda")
+    out = out_buf[1:].view(T, D)
+    ids = inputs.uniform_ids(rng, T, V)
+    mole.mole_embed_forward(dev(ids), E, 2.0, out=out)
+    assert mole.mole_check() == 0
+    assert torch.equal(out, (E[dev(ids).long()] * 2.0).to(BF16)) and float(out_buf[0]) == 7.0
+
+
+def test_forward_table_beyond_2_31_elements(mole):
+    # row offsets pass 32 bits: 2^31 + elements of bf16
+    V, D = 1048600, 2056
+    E = torch.empty((V, D), dtype=BF16, device="cuda")
+    ids = torch.tensor([0, 1, V - 1, V - 2, 1044500], dtype=torch.int32, device="cuda")
+    E[ids.long()] = torch.arange(5, device="cuda", dtype=BF16)[:, None] + 1
+    out = mole.mole_embed_forward(ids, E, 1.0)
+    assert mole.mole_check() == 0
+    assert torch.equal(out, E[ids.long()])
+
+
+def _check_backward(mole, rng, T, V, D, dtype, ids, scale=1.3, dout=None):
+    dout = _rand(rng, T, D, dtype=dtype) if dout is None else dout
+    dE = _rand(rng, V, D)
+    start = dE.clone()
+    again = dE.clone()
+    mole.mole_embed_backward(dev(ids), dout, dE, scale)
+    mole.mole_embed_backward(dev(ids), dout, again, scale)
+    bad = bool(((ids < 0) | (ids >= V)).any())
+    assert mole.mole_check() == (5 if bad else 0)
+    want, bound = ref.embed_backward(ids, ref.f64(dout), ref.f64(start), float(np.float32(scale)), V)
+    ref.assert_within(ref.f64(dE), want, bound)
+    assert torch.equal(dE, again), "two runs differ"
+    untouched = np.setdiff1d(np.arange(V), ids)
+    assert torch.equal(dE[dev(untouched)], start[dev(untouched)])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,V,D,kind", [
+    (1, 1, 1, "uniform"), (1, 50304, 64, "zipf"), (2, 1, 24, "uniform"),   # a key of one bit, one token
+    (31, 5, 40, "uniform"), (257, 300, 1001, "zipf"),                      # odd width: scalar columns
+    (1000, 40, 512, "uniform"),                                           # every run crosses chunks
+    (3001, 70000, 136, "zipf"),                                           # three digits of key
+    (5000, 300, 2056, "zipf"), (9999, 2, 72, "uniform"),
+    (20000, 50304, 256, "zipf"),
+])
+def test_backward(mole, T, V, D, kind, dtype):
+    rng = np.random.default_rng(T * 7 + V)
+    _check_backward(mole, rng, T, V, D, dtype, inputs.draw_ids(rng, T, V, kind))
+
+
+@pytest.mark.parametrize("T", [1, 15, 16, 17, 32, 33, 4096, 40000])
+def test_backward_one_id(mole, T):
+    # all tokens one id: a single run over every chunk
+    rng = np.random.default_rng(T)
+    _check_backward(mole, rng, T, 9, 64, F32, np.full(T, 4, np.int32))
+
+
+def test_backward_runs_that_end_on_chunk_borders(mole):
+    # runs of exactly 16 and 32 tokens: nothing crosses, every chunk is one run
+    rng = np.random.default_rng(3)
+    ids = np.repeat(np.arange(40), 16).astype(np.int32)
+    _check_backward(mole, rng, ids.size, 50, 64, F32, rng.permutation(ids))
+    ids = np.repeat(np.arange(21), 32).astype(np.int32)
+    _check_backward(mole, rng, ids.size, 21, 64, BF16, rng.permutation(ids))
+
+
+def test_backward_bad_ids(mole):
+    rng = np.random.default_rng(4)
+    T, V, D = 777, 60, 96
+    ids = inputs.uniform_ids(rng, T, V)
+    ids[::5] = -1
+    ids[3::50] = V
+    ids[4::70] = 2 ** 31 - 1
+    _check_backward(mole, rng, T, V, D, F32, ids)
+    _check_backward(mole, rng, T, V, D, BF16, np.full(T, -7, np.int32))  # none left
+
+
+def test_backward_bad_tokens_do_not_spread(mole):
+    # NaN and infinite rows of tokens with bad ids reach nothing
+    rng = np.random.default_rng(5)
+    T, V, D = 200, 30, 64
+    ids = inputs.uniform_ids(rng, T, V)
+    ids[:50] = -1
+    dout = _rand(rng, T, D)
+    dout[:25] = float("nan")
+    dout[25:50] = float("inf")
+    dE = torch.zeros(V, D, device="cuda")
+    mole.mole_embed_backward(dev(ids), dout, dE)
+    assert mole.mole_check() == 5
+    want, bound = ref.embed_backward(ids[50:], ref.f64(dout)[50:], np.zeros((V, D)), 1.0, V)
+    ref.assert_within(ref.f64(dE), want, bound)
+
+
+def test_backward_from_unaligned_rows(mole):
+    rng = np.random.default_rng(6)
+    T, V, D = 90, 20, 64
+    ids = inputs.zipf_ids(rng, T, V)
+    dout = _rand(rng, T * D + 1, dtype=BF16)[1:].view(T, D)
+    _check_backward(mole, rng, T, V, D, BF16, ids, dout=dout)
+    buf = torch.zeros(V * D + 2, device="cuda")
+    mole.mole_embed_backward(dev(ids), dout, buf[1:-1].view(V, D))
+    assert mole.mole_check() == 0
+    want, bound = ref.embed_backward(ids, ref.f64(dout), np.zeros((V, D)), 1.0, V)
+    ref.assert_within(ref.f64(buf[1:-1]).reshape(V, D), want, bound)
+    assert float(buf[0]) == 0.0 and float(buf[-1]) == 0.0
+
+
+def test_backward_large_batch_and_vocabulary(mole):
+    # 200000 tokens over 2^24 + ids (four digits of key), checked by torch in fp64
+    rng = np.random.default_rng(7)
+    T, V, D = 200000, (1 << 24) + 5, 8
+    ids = inputs.uniform_ids(rng, T, V)
+    ids[:5000] = V - 1
+    dout = _rand(rng, T, D)
+    dE = torch.zeros(V, D, device="cuda")
+    mole.mole_embed_backward(dev(ids), dout, dE)
+    assert mole.mole_check() == 0
+    want = torch.zeros(V, D, dtype=torch.float64, device="cuda").index_add_(0, dev(ids), dout.double())
+    mag = torch.zeros(V, D, dtype=torch.float64, device="cuda").index_add_(0, dev(ids), dout.double().abs())
+    assert bool(((dE.double() - want).abs() <= 5004 * ref.U * mag).all())
+
+
+def test_backward_on_a_stream_and_in_a_graph(mole):
+    rng = np.random.default_rng(8)
+    T, V, D = 3000, 500, 128
+    ids, dout = dev(inputs.zipf_ids(rng, T, V)), _rand(rng, T, D)
+    want = mole.mole_embed_backward(ids, dout, torch.zeros(V, D, device="cuda"))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = mole.mole_embed_backward(ids, dout, torch.zeros(V, D, device="cuda"), stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    # captured once, replayed on new inputs in the same buffers
+    dE, out = torch.zeros(V, D, device="cuda"), torch.empty(T, D, device="cuda")
+    E = _rand(rng, V, D)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mole.mole_embed_forward(ids, E, 2.0, out=out)
+        mole.mole_embed_backward(ids, dout, dE)
+    for seed in (1, 2):
+        rng = np.random.default_rng(seed)
+        ids.copy_(dev(inputs.zipf_ids(rng, T, V)))
+        dout.copy_(_rand(rng, T, D))
+        dE.zero_()
+        graph.replay()
+        assert torch.equal(out, E[ids.long()] * 2.0)
+        assert torch.equal(dE, mole.mole_embed_backward(ids, dout, torch.zeros(V, D, device="cuda")))
+    assert mole.mole_check() == 0
+
+
+def test_empty_batch(mole):
+    E = torch.ones(4, 8, device="cuda")
+    ids = torch.empty(0, dtype=torch.int32, device="cuda")
+    assert mole.mole_embed_forward(ids, E).shape == (0, 8)
+    dE = torch.ones(4, 8, device="cuda")
+    mole.mole_embed_backward(ids, torch.empty(0, 8, device="cuda"), dE)
+    assert mole.mole_check() == 0 and bool((dE == 1).all())
