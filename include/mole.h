@@ -395,8 +395,9 @@ mole_status mole_train_backward(const int32_t* ids, int64_t T, const void* group
  *       return; calls that share one must not overlap on the GPU.
  *
  * Both take any D up to 2^20 and T up to 2^31 - 1 (T == 0 is a no-op), and
- * pointers aligned to their element; 16-byte aligned pointers with D a
- * multiple of 8 take the vector kernels.
+ * pointers aligned to their element; rows that start on 4 elements (D a
+ * multiple of 4, pointers aligned to 16 bytes, bf16 ones to 8) take the vector
+ * kernels.
  */
 mole_status mole_embed_forward(const int32_t* ids, int64_t T, const void* E, int64_t V, int64_t D, float scale,
                                mole_dtype dt_E, void* out, mole_dtype dt_out, cudaStream_t stream);
@@ -434,8 +435,9 @@ mole_status mole_embed_backward(const int32_t* ids, int64_t T, const void* dout,
  * dw_post only; calls that share one must not overlap on the GPU.
  *
  * Both take any D up to 8192 and T up to 2^31 - 1 (T == 0 is a no-op), and
- * pointers aligned to their element; 16-byte aligned pointers with D a
- * multiple of 8 take the vector kernels.
+ * pointers aligned to their element; rows that start on 4 elements (D a
+ * multiple of 4, pointers aligned to 16 bytes, bf16 ones to 8) take the vector
+ * kernels.
  */
 mole_status mole_block_norm_forward(const void* x, mole_dtype dt_x, const void* f, mole_dtype dt_f,
                                     const float* w_post, const float* gate, float res_scale, const float* w_pre,

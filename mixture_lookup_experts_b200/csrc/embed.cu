@@ -9,13 +9,14 @@
 // (one of 50304 ids takes one token in seven of a Zipf batch), so the work is
 // split over the tokens in id order, not over the ids:
 //   1. embed_sort_kernel: (id, t) sorted by id, stably (ascending t inside an
-//      id), by a radix sort of 8-bit digits run by ONE cluster of 8 CTAs: the
-//      digit counts of its 256 warps meet in distributed shared memory, so a
+//      id), by a radix sort of 8-bit digits run by ONE cluster of 16 CTAs: the
+//      digit counts of its 512 warps meet in distributed shared memory, so a
 //      pass costs two cluster barriers instead of two kernel boundaries.
 //   2. embed_chunk_kernel: fixed chunks of the sorted order, one group of
-//      threads per (chunk, slice of columns); runs of equal ids inside a chunk
-//      go to dE, the runs that cross a chunk border leave partial sums.
-//   3. embed_join_kernel: per crossing run, its partial sums in chunk order.
+//      threads per (chunk, slice of columns); the runs of equal ids go to dE,
+//      but those longer than a chunk leave partial sums.
+//   3. embed_join_kernel: per long run, its partial sums in chunk order.
+// Batches of up to kSmallTokens do all of it in one launch (embed_small_kernel).
 // Every sum has one order, fixed by the ids alone: the result has the same
 // bits on every run.
 #include <cooperative_groups.h>
@@ -28,37 +29,51 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kEmbedThreads = 256;
-constexpr int kSortCtas = 8;
+constexpr int kSortCtas = 16;  // 16 measured against 8: 12.1 -> 11.6 us at 16384 tokens, 37 -> 24 at 65536
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDigits = 256;
 constexpr int kChunkThreads = 128;
-constexpr int kRowsInFlight = 8;
+constexpr int kJoinThreads = 128;
+constexpr int kChunkUnits = 2, kChunkSlots = 5, kScalarCols = 8;
+constexpr int64_t kChunkGroups = 1776;  // chunks times slices: 12 CTAs for each of 148 SMs
+constexpr int kSmallTokens = 2048;
 
 // ---- forward ----
-// blockDim = (tx, 256 / tx): a row slice per group, rows in grid order.
-template <bool kVec, class In, class Out>
+// blockDim = (tx, 256 / tx): a row slice per group of tx threads, kRows rows in
+// flight each (their ids are loaded together, then their rows: two waits for
+// memory per kRows rows).
+template <bool kVec, class In, class Out, int kRows>
 __global__ void __launch_bounds__(kEmbedThreads) embed_forward_kernel(const int32_t* __restrict__ ids, int64_t T,
                                                                       const In* __restrict__ E, int64_t V, int D,
                                                                       float scale, Out* __restrict__ out,
                                                                       unsigned* err) {
   const int tx = blockDim.x;
   const int slice0 = blockIdx.y * tx * 8;
-  const int col0 = kVec ? slice0 + 8 * threadIdx.x : slice0 + threadIdx.x;
+  const int col0 = slice0 + (kVec ? 4 : 1) * (int)threadIdx.x;
   if (col0 >= D) return;
-  for (int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; t < T; t += (int64_t)gridDim.x * blockDim.y) {
-    const int32_t id = __ldg(ids + t);
+  const int64_t t0 = ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * kRows;
+  int32_t id[kRows];
+  RowUnit<kVec, In, 8> row[kRows];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) id[r] = t0 + r < T ? __ldg(ids + t0 + r) : 0;
+#pragma unroll
+  for (int r = 0; r < kRows; ++r)
+    if (t0 + r < T && id[r] >= 0 && (int64_t)id[r] < V) row[r].load(E + (int64_t)id[r] * D, col0, tx, D);
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    if (t0 + r >= T) return;
     float f[8];
-    if (id < 0 || (int64_t)id >= V) {
+    if (id[r] >= 0 && (int64_t)id[r] < V) {
+      row[r].get(f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] *= scale;
+    } else {
       if (threadIdx.x == 0 && blockIdx.y == 0) atomicOr(err, kErrIndex);
 #pragma unroll
       for (int k = 0; k < 8; ++k) f[k] = NAN;
-    } else {
-      ld_cols<kVec>(E + (int64_t)id * D, col0, tx, D, f);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] *= scale;
     }
-    st_cols<kVec>(out + t * D, col0, tx, D, f);
+    st_cols<kVec>(out + (t0 + r) * D, col0, tx, D, f);
   }
 }
 
@@ -66,100 +81,186 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_forward_kernel(const int3
 struct SortArgs {
   const int32_t* ids;
   int64_t T, V;
-  int2* buf[2];  // {id, t}; the last pass writes buf[0]
+  int2* to;      // {id, t}: the sorted elements
+  int2* other;   // the second buffer of the global passes, which end in `to`
   int passes;
+  int* n_runs;   // cleared for the chunk kernel
   unsigned* err;
 };
 
-// Key of a bad id: V, behind every row (keys fit 31 bits + 1: V <= 2^31 - 1).
-__device__ __forceinline__ int2 sort_input(const SortArgs& a, int pass, int64_t i) {
-  if (pass == 0) {
-    const int32_t id = __ldg(a.ids + i);
-    const bool ok = id >= 0 && (int64_t)id < a.V;
-    return make_int2(ok ? id : (int)a.V, (int)i);
-  }
-  return __ldcg(a.buf[(a.passes - pass) & 1] + i);  // another CTA wrote it: past L1
+// Key of a bad id: V, behind every row (keys fit 31 bits: V <= 2^31 - 1).
+__device__ __forceinline__ int2 sort_key(const int32_t* ids, int64_t V, int64_t i) {
+  const int32_t id = __ldg(ids + i);
+  return make_int2(id >= 0 && (int64_t)id < V ? id : (int)V, (int)i);
 }
 
+// Digits and counts of a radix pass run by one CTA (of kSortWarps warps).
+struct SortSmem {
+  int hist[kSortWarps][kDigits];  // per warp: its count of a digit, then its offset inside the CTA
+  int psum[kSortThreads / kDigits][kDigits];
+  int tot[kDigits];               // per digit: the CTA's count
+  int base[kDigits];              // per digit: position of the CTA's first element
+  int wsum[kDigits / 32];
+};
+
+// Ranks of a warp's tiles e[j] (elements 32 j + lane < n of its range) among
+// the elements of equal digit that the warp has seen; hist counts on.  The
+// lanes of equal digit come from one ballot per bit (__match_any_sync took
+// 1.1 us a tile with 32 warps on the SM).
+template <int kHold>
+__device__ __forceinline__ void rank_tiles(const int2 (&e)[kHold], int (&rank)[kHold], int64_t n, int shift,
+                                           int* hist) {
+  const int lane = threadIdx.x & 31;
+  const unsigned lower = (1u << lane) - 1u;
+#pragma unroll
+  for (int j = 0; j < kHold; ++j) {
+    if (32 * j >= n) break;
+    const bool in = 32 * j + lane < n;
+    const int d = in ? ((unsigned)e[j].x >> shift) & (kDigits - 1) : 0;
+    unsigned same = __ballot_sync(0xffffffffu, in);  // the lanes of this lane's digit
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      const unsigned ones = __ballot_sync(0xffffffffu, (d >> b) & 1);
+      same &= (d >> b) & 1 ? ones : ~ones;
+    }
+    const int off = hist[d];
+    __syncwarp();
+    if (in) {
+      rank[j] = off + __popc(same & lower);
+      if ((same & lower) == 0) hist[d] = off + __popc(same);
+    }
+    __syncwarp();
+  }
+}
+
+// hist (counts per warp) to offsets inside the CTA, and the totals.
+__device__ __forceinline__ void scan_warps(SortSmem& s) {
+  constexpr int kParts = kSortThreads / kDigits, kPartWarps = kSortWarps / kParts;
+  const int digit = threadIdx.x & (kDigits - 1), part = threadIdx.x / kDigits;
+  int c[kPartWarps], run = 0;
+#pragma unroll
+  for (int w = 0; w < kPartWarps; ++w) {
+    c[w] = run;
+    run += s.hist[part * kPartWarps + w][digit];
+  }
+  s.psum[part][digit] = run;
+  __syncthreads();
+  int start = 0;
+#pragma unroll
+  for (int p = 0; p < kParts; ++p)
+    if (p < part) start += s.psum[p][digit];
+#pragma unroll
+  for (int w = 0; w < kPartWarps; ++w) s.hist[part * kPartWarps + w][digit] = start + c[w];
+  if (part == kParts - 1) s.tot[digit] = start + run;
+}
+
+// base[d] = sum of `all` over the digits before d, plus `before` (threads below
+// kDigits hold their digit's values).
+__device__ __forceinline__ void scan_digits(SortSmem& s, int all, int before) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = all;
+  if (threadIdx.x < kDigits) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) s.wsum[warp] = incl;
+  }
+  __syncthreads();
+  if (threadIdx.x < kDigits) {
+    int off = incl - all + before;
+#pragma unroll
+    for (int w = 0; w < kDigits / 32; ++w)
+      if (w < warp) off += s.wsum[w];
+    s.base[threadIdx.x] = off;
+  }
+  __syncthreads();
+}
+
+// Where the sort's elements live between passes: while a CTA's share fits its
+// shared memory (kHold > 0: kHold tiles of 32 a warp, held in registers inside
+// a pass) the passes exchange them through distributed shared memory, else
+// through the two global buffers, in batches of 8 tiles.
+template <int kHold>
 __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads, 1)
     embed_sort_kernel(const SortArgs a) {
-  __shared__ int hist[kSortWarps][kDigits];  // per warp: its count of a digit, then its offset inside the CTA
-  __shared__ int tot[kDigits];               // per digit: the CTA's count (read by the cluster)
-  __shared__ int base[kDigits];              // per digit: first position of the CTA's elements
-  __shared__ int wsum[kDigits / 32];
+  constexpr bool kLocal = kHold > 0;
+  constexpr int H = kLocal ? kHold : 8;
+  extern __shared__ __align__(16) uint8_t sort_smem[];
+  SortSmem& s = *reinterpret_cast<SortSmem*>(sort_smem);
+  int2* mine = reinterpret_cast<int2*>(sort_smem + sizeof(SortSmem));  // kLocal: this CTA's elements
   pdl_trigger();  // the chunk kernel may take its place on the other SMs
   cg::cluster_group cluster = cg::this_cluster();
   const int cta = (int)cluster.block_rank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (cta == 0 && threadIdx.x == 0) *a.n_runs = 0;
   // each warp owns a contiguous range of the input, so that warp order is input order
-  const int64_t per = ((a.T + kSortCtas * kSortWarps - 1) / (kSortCtas * kSortWarps) + 31) / 32 * 32;
+  const int64_t per = kLocal ? 32 * H : ((a.T + kSortCtas * kSortWarps - 1) / (kSortCtas * kSortWarps) + 31) / 32 * 32;
   const int64_t lo = std::min<int64_t>(a.T, per * (cta * kSortWarps + warp));
   const int64_t hi = std::min<int64_t>(a.T, lo + per);
   for (int pass = 0; pass < a.passes; ++pass) {
     const int shift = 8 * pass;
-    for (int d = lane; d < kDigits; d += 32) hist[warp][d] = 0;
-    __syncwarp();
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-      const bool in = i0 + lane < hi;
-      const unsigned act = __ballot_sync(0xffffffffu, in);
-      if (in) {
-        const int2 e = sort_input(a, pass, i0 + lane);
-        if (pass == 0 && (int64_t)e.x == a.V) atomicOr(a.err, kErrIndex);
-        const int d = ((unsigned)e.x >> shift) & (kDigits - 1);
-        const unsigned same = __match_any_sync(act, d);
-        if (lane == __ffs(same) - 1) hist[warp][d] += __popc(same);
+    const bool last = pass == a.passes - 1;
+    int2 e[H];
+    int rank[H];
+    auto load = [&](int64_t i0) {
+#pragma unroll
+      for (int j = 0; j < H; ++j) {
+        const int64_t i = i0 + 32 * j + lane;
+        if (i >= hi) continue;
+        if (pass == 0)
+          e[j] = sort_key(a.ids, a.V, i);
+        else if (kLocal)
+          e[j] = mine[i - per * kSortWarps * cta];
+        else
+          e[j] = __ldcg(((a.passes - pass) & 1 ? a.other : a.to) + i);  // another CTA wrote it: past L1
       }
-      __syncwarp();
+    };
+    for (int d = lane; d < kDigits; d += 32) s.hist[warp][d] = 0;
+    __syncwarp();
+    for (int64_t i0 = lo; i0 < hi; i0 += 32 * H) {
+      load(i0);
+      if (pass == 0) {
+#pragma unroll
+        for (int j = 0; j < H; ++j)
+          if (i0 + 32 * j + lane < hi && (int64_t)e[j].x == a.V) atomicOr(a.err, kErrIndex);
+      }
+      rank_tiles<H>(e, rank, hi - i0, shift, s.hist[warp]);
     }
     __syncthreads();
+    scan_warps(s);
+    cluster.sync();  // tot is there (and every element of `mine` is in registers)
+    int before = 0, all = 0;
     if (threadIdx.x < kDigits) {
-      int run = 0;
-      for (int w = 0; w < kSortWarps; ++w) {
-        const int c = hist[w][threadIdx.x];
-        hist[w][threadIdx.x] = run;
-        run += c;
-      }
-      tot[threadIdx.x] = run;
-    }
-    cluster.sync();
-    int before = 0, all = 0, incl = 0;
-    if (threadIdx.x < kDigits) {
-      for (int c = 0; c < kSortCtas; ++c) {
-        const int x = cluster.map_shared_rank(tot, c)[threadIdx.x];
-        if (c < cta) before += x;
+#pragma unroll
+      for (int r = 0; r < kSortCtas; ++r) {
+        const int x = cluster.map_shared_rank(s.tot, r)[threadIdx.x];
+        if (r < cta) before += x;
         all += x;
       }
-      incl = all;
+    }
+    scan_digits(s, all, before);
+    int2* dst = (a.passes - 1 - pass) & 1 ? a.other : a.to;
+    for (int64_t i0 = lo; i0 < hi; i0 += 32 * H) {
+      if (!kLocal) {  // hist runs on from the warp's offset: rank counts from the CTA's first element
+        load(i0);
+        rank_tiles<H>(e, rank, hi - i0, shift, s.hist[warp]);
+      }
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
+      for (int j = 0; j < H; ++j) {
+        if (i0 + 32 * j + lane >= hi) continue;
+        const int d = ((unsigned)e[j].x >> shift) & (kDigits - 1);
+        const int pos = s.base[d] + rank[j] + (kLocal ? s.hist[warp][d] : 0);
+        if (kLocal && !last) {
+          const int share = 32 * H * kSortWarps;
+          cluster.map_shared_rank(mine, pos / share)[pos % share] = e[j];
+        } else {
+          __stcg(dst + pos, e[j]);
+        }
       }
-      if (lane == 31) wsum[warp] = incl;
     }
-    __syncthreads();
-    if (threadIdx.x < kDigits) {
-      int off = incl - all + before;
-      for (int w = 0; w < warp; ++w) off += wsum[w];
-      base[threadIdx.x] = off;
-    }
-    __syncthreads();
-    int2* dst = a.buf[(a.passes - 1 - pass) & 1];
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-      const bool in = i0 + lane < hi;
-      const unsigned act = __ballot_sync(0xffffffffu, in);
-      if (in) {
-        const int2 e = sort_input(a, pass, i0 + lane);
-        const int d = ((unsigned)e.x >> shift) & (kDigits - 1);
-        const unsigned same = __match_any_sync(act, d);
-        const int off = hist[warp][d];
-        __syncwarp(act);
-        if (lane == __ffs(same) - 1) hist[warp][d] = off + __popc(same);
-        __stcg(dst + base[d] + off + __popc(same & ((1u << lane) - 1u)), e);
-      }
-      __syncwarp();
-    }
-    // the pass's output (global) and the readers of tot are done
+    // the pass's output and the readers of tot are done
     cluster.sync();
   }
 }
@@ -174,123 +275,390 @@ struct SumArgs {
   float scale;
   float* dE;
   float* part;  // [n_chunks][2][D]: sums of the run that enters the chunk, of the run that leaves it
+  int* n_runs;      // runs with parts: how many,
+  int2* runs;       // and of each {chunk where it begins, id}, in any order
 };
 
-template <bool kVec>
-__device__ __forceinline__ void add_row(float* row, int col0, int step, int D, float scale, const float (&acc)[8]) {
-  float f[8];
-  ld_cols<kVec>(row, col0, step, D, f);
+// Rows of dout in order of their runs: batches of kQ tokens have the loads of
+// their rows in flight, and with them those rows of dE whose run ends in the
+// batch (a load inside the sums would stall them once per run).  kAhead: the
+// ids of the next batch are loaded meanwhile.  `at(p)` gives the sorted element p, p < end
+// only; `whole` takes a run that both begins and ends in [p0, p1), `head` the
+// sum of one that entered, `tail` of one that leaves.
+template <bool kVec, class In, int C, int kQ, bool kAhead, class At, class Head, class Tail>
+__device__ __forceinline__ void sum_runs(const In* dout, float* dE, int D, float scale, int V, int64_t p0, int64_t p1,
+                                         int64_t end, int enters, int col0, int step, At at, Head head, Tail tail) {
+  float acc[C];
+  int cur = -1;
+  int2 e[kQ + 1];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) f[k] = fmaf(scale, acc[k], f[k]);
-  st_cols<kVec>(row, col0, step, D, f);
+  for (int q = 0; q <= kQ; ++q) e[q] = p0 + q < end ? at(p0 + q) : make_int2(-1, 0);
+  for (int64_t p = p0; p < p1; p += kQ) {
+    RowUnit<kVec, In, C> row[kQ];
+    RowUnit<kVec, float, C> grad[kQ];
+#pragma unroll
+    for (int q = 0; q < kQ; ++q)
+      if (p + q < p1 && e[q].x != V) {
+        row[q].load(dout + (int64_t)e[q].y * D, col0, step, D);
+        if (e[q].x != e[q + 1].x && e[q].x != enters) grad[q].load(dE + (int64_t)e[q].x * D, col0, step, D);
+      }
+    int2 next[kAhead ? kQ + 1 : 1];
+    if constexpr (kAhead) {
+      next[0] = e[kQ];
+#pragma unroll
+      for (int q = 1; q <= kQ; ++q) next[q] = p + kQ + q < end ? at(p + kQ + q) : make_int2(-1, 0);
+    }
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) {
+      if (p + q >= p1 || e[q].x == V) break;
+      float f[C];
+      row[q].get(f);
+#pragma unroll
+      for (int k = 0; k < C; ++k) acc[k] = e[q].x == cur ? acc[k] + f[k] : f[k];
+      cur = e[q].x;
+      const bool ends = e[q].x != e[q + 1].x;
+      if (cur == enters) {
+        if (ends || p + q + 1 == p1) head(acc);
+      } else if (ends) {
+        float g[C];
+        grad[q].get(g);
+#pragma unroll
+        for (int k = 0; k < C; ++k) g[k] = fmaf(scale, acc[k], g[k]);
+        st_cols<kVec>(dE + (int64_t)cur * D, col0, step, D, g);
+      } else if (p + q + 1 == p1) {
+        tail(cur, acc);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q <= kQ; ++q) {
+      if constexpr (kAhead)
+        e[q] = next[q];
+      else
+        e[q] = p + kQ + q < end ? at(p + kQ + q) : make_int2(-1, 0);
+    }
+  }
 }
 
-// blockDim = (tx, 128 / tx): threadIdx.y = chunk inside the CTA, blockIdx.y = slice.
-template <bool kVec, class In>
+// Step 2.  blockDim = (tx, 128 / tx): threadIdx.y = chunk inside the CTA,
+// blockIdx.y = slice of columns.  A chunk's share is its own tokens, with one
+// change at each border so that only runs longer than a chunk have parts: a run
+// that crosses one border belongs whole to the chunk where it begins.
+struct Share {
+  int begin, end;      // tokens of the share, from the chunk's first one; end may pass the chunk
+  int enters, leaves;  // ids (or -1): of a part that entered the chunk, of one that leaves it
+};
+
+// `id(i)`: id of the i-th token from the chunk's first, -1 outside the batch,
+// for i from -chunk - 1 to 2 * chunk; n tokens in the chunk.
+template <class Id>
+__device__ __forceinline__ Share chunk_share(int n, int chunk, Id id) {
+  Share s{0, n, -1, -1};
+  const int first = id(0), last = id(n - 1);
+  if (id(-1) == first) {
+    // one border crossed: it begins in the chunk before this one and ends here
+    if (id(-chunk - 1) != first && id(chunk) != first) {
+      while (s.begin < n && id(s.begin) == first) ++s.begin;
+    } else {
+      s.enters = first;
+    }
+  }
+  if (n == chunk && id(n) == last && s.enters != last) {
+    if (id(2 * chunk) == last)
+      s.leaves = last;
+    else
+      while (id(s.end) == last) ++s.end;
+  }
+  return s;
+}
+
+__device__ __forceinline__ void leave_run(const SumArgs& a, int64_t c, int id) {
+  if (threadIdx.x == 0 && blockIdx.y == 0) a.runs[atomicAdd(a.n_runs, 1)] = make_int2((int)c, id);
+}
+
+// Vector rows: a thread streams its columns of the chunk's rows through a ring
+// of kSlots slots of its own in shared memory (cp.async; nothing is shared
+// between threads), so that kSlots rows are in flight per thread whatever the
+// registers; with a row come the columns of dE where its run ends.  A thread
+// has kUnits units of 4 columns, 4 * blockDim.x apart: accesses to dout and to
+// dE are both contiguous over a warp, and the bookkeeping of a token serves all
+// of them.
+template <class In, int kUnits, int kSlots>
 __global__ void __launch_bounds__(kChunkThreads) embed_chunk_kernel(const SumArgs a) {
+  constexpr int kIn = 4 * sizeof(In), kUnitBytes = kIn + 16, kSlotBytes = kUnits * kUnitBytes * kChunkThreads;
+  extern __shared__ __align__(16) uint8_t chunk_smem[];
+  // slot: per unit the threads' columns of dout, then their columns of dE
+  const int tid = threadIdx.y * blockDim.x + threadIdx.x;
+  // the tokens of the chunk and of the next one (es[0] .. es[2 * chunk - 1]), and
+  // those at -1, -chunk - 1 and 2 * chunk
+  int2* es = reinterpret_cast<int2*>(chunk_smem + (size_t)kSlots * kSlotBytes) +
+             (size_t)threadIdx.y * (2 * a.chunk + 3) + 2;
   pdl_trigger();
   const int64_t c = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const int step = blockDim.x;
-  const int col0 = blockIdx.y * step * 8 + (kVec ? 8 : 1) * (int)threadIdx.x;
+  const int col0 = blockIdx.y * step * 4 * kUnits + 4 * (int)threadIdx.x;
+  const int64_t p0 = c * a.chunk;
+  const int n = c < a.n_chunks ? (int)std::min<int64_t>(a.chunk, a.T - p0) : 0;
   pdl_wait();
-  if (c >= a.n_chunks || col0 >= a.D) return;
-  const In* dout = static_cast<const In*>(a.dout);
-  const int64_t p0 = c * a.chunk, p1 = std::min<int64_t>(a.T, p0 + a.chunk);
-  const int V = (int)a.V;
-  const int enters = c > 0 ? a.sorted[p0 - 1].x : -1;   // id of the run that may enter the chunk
-  const int leaves = p1 < a.T ? a.sorted[p1].x : -1;     // id of the run that may leave it
-  float acc[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) acc[k] = 0.f;
-  int cur = a.sorted[p0].x;
-  bool entered = cur == enters;
-  auto flush = [&](bool at_end) {
-    if (cur == V) return;
-    float* part = a.part + 2 * c * a.D;
-    if (entered)
-      st_cols<kVec>(part, col0, step, a.D, acc);
-    else if (at_end && cur == leaves)
-      st_cols<kVec>(part + a.D, col0, step, a.D, acc);
-    else
-      add_row<kVec>(a.dE + (int64_t)cur * a.D, col0, step, a.D, a.scale, acc);
-  };
-  for (int64_t p = p0; p < p1; p += kRowsInFlight) {
-    int2 e[kRowsInFlight];
-    float f[kRowsInFlight][8];
-#pragma unroll
-    for (int q = 0; q < kRowsInFlight; ++q) e[q] = p + q < p1 ? a.sorted[p + q] : make_int2(V, 0);
-#pragma unroll
-    for (int q = 0; q < kRowsInFlight; ++q)
-      if (e[q].x != V) ld_cols<kVec>(dout + (int64_t)e[q].y * a.D, col0, step, a.D, f[q]);
-#pragma unroll
-    for (int q = 0; q < kRowsInFlight; ++q) {
-      if (p + q >= p1) break;
-      if (e[q].x != cur) {
-        flush(false);
-        cur = e[q].x;
-        entered = false;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] = 0.f;
-      }
-      if (cur != V)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] += f[q][k];
+  if (n > 0)
+    for (int i = (int)threadIdx.x - 2; i <= 2 * a.chunk; i += step) {
+      const int64_t p = i == -2 ? p0 - a.chunk - 1 : p0 + i;
+      es[i] = p >= 0 && p < a.T ? a.sorted[p] : make_int2(-1, 0);
     }
+  __syncthreads();
+  if (n == 0 || col0 >= a.D) return;
+  const Share share = chunk_share(n, a.chunk, [&](int i) { return es[i < -1 ? -2 : i].x; });
+  const int units = std::min(kUnits, (a.D - col0 + 4 * step - 1) / (4 * step));  // those that begin inside the row
+  const In* dout = static_cast<const In*>(a.dout) + col0;
+  float* dE = a.dE + col0;
+  const int V = (int)a.V;
+  float* part = a.part + 2 * c * a.D + col0;
+  auto fetch = [&](int i, int at) {
+    if (i < share.end && es[i].x != V) {
+      uint8_t* slot = chunk_smem + at * kSlotBytes;
+      const int2 e = es[i];
+      const In* row = dout + (int64_t)e.y * a.D;
+      const bool whole = e.x != es[i + 1].x && e.x != share.enters;
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u)
+        if (u < units) {
+          cp_async<kIn>(slot + (u * kChunkThreads + tid) * kIn, row + u * 4 * step);
+          if (whole)
+            cp_async<16>(slot + kUnits * kChunkThreads * kIn + (u * kChunkThreads + tid) * 16,
+                         dE + (int64_t)e.x * a.D + u * 4 * step);
+        }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kSlots - 1; ++i) fetch(share.begin + i, i);
+  float acc[kUnits][4];
+  int cur = -1, at = 0;
+  for (int i = share.begin; i < share.end; ++i) {
+    const int id = es[i].x;
+    if (id == V) break;
+    fetch(i + kSlots - 1, at == 0 ? kSlots - 1 : at - 1);
+    cp_async_wait<kSlots - 1>();
+    const uint8_t* slot = chunk_smem + at * kSlotBytes;
+    at = at + 1 == kSlots ? 0 : at + 1;
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      float f[4];
+      ld_unit(reinterpret_cast<const In*>(slot + (u * kChunkThreads + tid) * kIn), f);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[u][k] = id == cur ? acc[u][k] + f[k] : f[k];
+    }
+    cur = id;
+    const bool ends = id != es[i + 1].x;
+    if (!ends && i + 1 != share.end) continue;
+    float* to = part;  // a part that entered
+    if (id != share.enters) {
+      if (ends) {
+        to = dE + (int64_t)id * a.D;
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+          const float4 x = *reinterpret_cast<const float4*>(slot + kUnits * kChunkThreads * kIn +
+                                                            (u * kChunkThreads + tid) * 16);
+          acc[u][0] = fmaf(a.scale, acc[u][0], x.x);
+          acc[u][1] = fmaf(a.scale, acc[u][1], x.y);
+          acc[u][2] = fmaf(a.scale, acc[u][2], x.z);
+          acc[u][3] = fmaf(a.scale, acc[u][3], x.w);
+        }
+      } else {
+        to = part + a.D;
+        leave_run(a, c, id);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u)
+      if (u < units) st_unit(to + u * 4 * step, acc[u][0], acc[u][1], acc[u][2], acc[u][3]);
   }
-  flush(true);
+  cp_async_wait<0>();
 }
 
-// One group of threads per (chunk, slice): where a run starts in the chunk and
-// leaves it, the sum of its parts.
-template <bool kVec>
-__global__ void __launch_bounds__(kChunkThreads) embed_join_kernel(const SumArgs a) {
+// Rows of any width and alignment.
+template <class In>
+__global__ void __launch_bounds__(kChunkThreads) embed_chunk_scalar_kernel(const SumArgs a) {
+  constexpr int C = kScalarCols, kQ = 4;
+  pdl_trigger();
   const int64_t c = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const int step = blockDim.x;
-  const int col0 = blockIdx.y * step * 8 + (kVec ? 8 : 1) * (int)threadIdx.x;
+  const int col0 = blockIdx.y * step * C + (int)threadIdx.x;
   pdl_wait();
-  if (c + 1 >= a.n_chunks || col0 >= a.D) return;
-  const int64_t next = (c + 1) * a.chunk;
-  const int id = a.sorted[next].x;
-  if (id == (int)a.V || a.sorted[next - 1].x != id) return;               // no run leaves this chunk
-  if (c > 0 && a.sorted[c * a.chunk - 1].x == id) return;                 // it began earlier
-  // the chunks that it enters: those after c whose first id is the run's
-  int64_t lo = c + 1, hi = a.n_chunks;  // first id of lo is the run's, of hi (if any) behind it
-  while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (a.sorted[mid * a.chunk].x == id)
-      lo = mid;
-    else
-      hi = mid;
+  if (c >= a.n_chunks || col0 >= a.D) return;
+  const int64_t p0 = c * a.chunk;
+  const Share share = chunk_share((int)std::min<int64_t>(a.chunk, a.T - p0), a.chunk, [&](int i) {
+    return p0 + i >= 0 && p0 + i < a.T ? a.sorted[p0 + i].x : -1;
+  });
+  float* part = a.part + 2 * c * a.D;
+  sum_runs<false, In, C, kQ, true>(
+      static_cast<const In*>(a.dout), a.dE, a.D, a.scale, (int)a.V, p0 + share.begin, p0 + share.end, a.T,
+      share.enters, col0, step, [&](int64_t p) { return a.sorted[p]; },
+      [&](const float(&acc)[C]) { st_cols<false>(part, col0, step, a.D, acc); },
+      [&](int id, const float(&acc)[C]) {
+        st_cols<false>(part + a.D, col0, step, a.D, acc);
+        leave_run(a, c, id);
+      });
+}
+
+// Number of chunks after c that the run of `id` enters (sorted ids: a prefix of
+// them), by a warp: 1024 chunks in two probes, 31 in one.
+__device__ __forceinline__ int64_t chunks_entered(const SumArgs& a, int64_t c, int id) {
+  const int lane = threadIdx.x & 31;
+  auto enters = [&](int64_t k) { return k < a.n_chunks && a.sorted[k * a.chunk].x == id; };
+  int64_t n = 0;  // chunks c + 1 .. c + n are entered
+  for (;;) {
+    const bool far = enters(c + n + 32 * (lane + 1)), near = enters(c + n + 1 + lane);
+    const int blocks = __popc(__ballot_sync(0xffffffffu, far)), rest = __popc(__ballot_sync(0xffffffffu, near));
+    if (blocks == 0) return n + rest;
+    n += 32 * blocks;
   }
-  float acc[8];
-  ld_cols<kVec>(a.part + (2 * c + 1) * a.D, col0, step, a.D, acc);
-  for (int64_t k0 = c + 1; k0 <= lo; k0 += kRowsInFlight) {
-    float f[kRowsInFlight][8];
+}
+
+// Step 3: the parts of the long runs, in chunk order, onto dE.  (The order of
+// the list of runs does not matter: each has its own row.)  Item = (run, 128
+// columns), a CTA each: its warps take the parts in contiguous shares, whose
+// sums are added in order.
+template <bool kVec>
+__global__ void __launch_bounds__(kJoinThreads, 8) embed_join_kernel(const SumArgs a) {
+  constexpr int C = 4, kWarpsJ = kJoinThreads / 32, kQ = 8;
+  __shared__ float sums[kWarpsJ][C][32];
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned slices = (a.D + 32 * C - 1) / (32 * C);
+  int2 r = a.runs[blockIdx.x / slices];  // with the count: used if there is such a run
+  const unsigned items = (unsigned)*a.n_runs * slices;
+  for (unsigned it = blockIdx.x; it < items; it += gridDim.x, r = it < items ? a.runs[it / slices] : r) {
+    const int col0 = (int)(it % slices) * 32 * C + (kVec ? C : 1) * lane;
+    const int64_t c = r.x;
+    float* to = a.dE + (int64_t)r.y * a.D;
+    RowUnit<kVec, float, C> grad;
+    if (warp == 0 && col0 < a.D) grad.load(to, col0, 32, a.D);
+    // part 0 left chunk c, part k entered chunk c + k
+    const int64_t n = 1 + chunks_entered(a, c, r.y);
+    const int64_t k1 = n * (warp + 1) / kWarpsJ;
+    float acc[C];
 #pragma unroll
-    for (int q = 0; q < kRowsInFlight; ++q)
-      if (k0 + q <= lo) ld_cols<kVec>(a.part + 2 * (k0 + q) * a.D, col0, step, a.D, f[q]);
+    for (int k = 0; k < C; ++k) acc[k] = 0.f;
+    if (col0 < a.D)
+      for (int64_t k0 = n * warp / kWarpsJ; k0 < k1; k0 += kQ) {
+        RowUnit<kVec, float, C> f[kQ];
 #pragma unroll
-    for (int q = 0; q < kRowsInFlight; ++q)
-      if (k0 + q <= lo)
+        for (int q = 0; q < kQ; ++q)
+          if (k0 + q < k1) f[q].load(a.part + (2 * (c + k0 + q) + (k0 + q == 0)) * a.D, col0, 32, a.D);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] += f[q][k];
+        for (int q = 0; q < kQ; ++q)
+          if (k0 + q < k1) {
+            float x[C];
+            f[q].get(x);
+#pragma unroll
+            for (int k = 0; k < C; ++k) acc[k] += x[k];
+          }
+      }
+#pragma unroll
+    for (int k = 0; k < C; ++k) sums[warp][k][lane] = acc[k];
+    __syncthreads();
+    if (warp == 0 && col0 < a.D) {
+      for (int w = 1; w < kWarpsJ; ++w)
+#pragma unroll
+        for (int k = 0; k < C; ++k) acc[k] += sums[w][k][lane];
+      float g[C];
+      grad.get(g);
+#pragma unroll
+      for (int k = 0; k < C; ++k) g[k] = fmaf(a.scale, acc[k], g[k]);
+      st_cols<kVec>(to, col0, 32, a.D, g);
+    }
+    __syncthreads();
   }
-  add_row<kVec>(a.dE + (int64_t)id * a.D, col0, step, a.D, a.scale, acc);
+}
+
+// ---- gradient of a small batch (T <= kSmallTokens): one launch ----
+// CTA = a strip of 32 columns, one a lane (any width and alignment).  Every CTA
+// sorts the whole batch in its shared memory (a few us; the other strips do the
+// same beside it), its 32 warps sum equal shares of the sorted tokens, and the
+// runs that cross a share are joined from shared memory.
+template <class In>
+__global__ void __launch_bounds__(kSortThreads, 1)
+    embed_small_kernel(const int32_t* __restrict__ ids, int T, int64_t V, int passes, const In* __restrict__ dout,
+                       int D, float scale, float* dE, unsigned* err) {
+  constexpr int H = kSmallTokens / kSortThreads, kQ = 8;
+  extern __shared__ __align__(16) uint8_t sort_smem[];
+  SortSmem& s = *reinterpret_cast<SortSmem*>(sort_smem);
+  int2* sorted = reinterpret_cast<int2*>(sort_smem + sizeof(SortSmem));  // [kSmallTokens]
+  float* part = reinterpret_cast<float*>(sorted + kSmallTokens);         // [kSortWarps][2][32]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lo = 32 * H * warp;
+  int2 e[H];
+  int rank[H];
+#pragma unroll
+  for (int j = 0; j < H; ++j) {
+    const int i = lo + 32 * j + lane;
+    if (i < T) {
+      e[j] = sort_key(ids, V, i);
+      if (blockIdx.x == 0 && (int64_t)e[j].x == V) atomicOr(err, kErrIndex);
+    }
+  }
+  for (int pass = 0; pass < passes; ++pass) {
+    for (int d = lane; d < kDigits; d += 32) s.hist[warp][d] = 0;
+    __syncwarp();
+    rank_tiles<H>(e, rank, T - lo, 8 * pass, s.hist[warp]);
+    __syncthreads();
+    scan_warps(s);
+    __syncthreads();
+    scan_digits(s, threadIdx.x < kDigits ? s.tot[threadIdx.x] : 0, 0);
+#pragma unroll
+    for (int j = 0; j < H; ++j)
+      if (lo + 32 * j + lane < T) {
+        const int d = ((unsigned)e[j].x >> (8 * pass)) & (kDigits - 1);
+        sorted[s.base[d] + s.hist[warp][d] + rank[j]] = e[j];
+      }
+    __syncthreads();
+    if (pass + 1 < passes) {
+#pragma unroll
+      for (int j = 0; j < H; ++j)
+        if (lo + 32 * j + lane < T) e[j] = sorted[lo + 32 * j + lane];
+    }
+  }
+  const int col = blockIdx.x * 32 + lane;
+  auto begin = [&](int w) { return (int)((int64_t)T * w / kSortWarps); };
+  const int p0 = begin(warp), p1 = begin(warp + 1);
+  float* entering = part + warp * 64 + lane;
+  float* leaving = entering + 32;
+  int owner = -1;  // the id of the run that begins in this share and leaves it
+  if (p0 < p1 && col < D)
+    sum_runs<false, In, 1, kQ, false>(
+        dout, dE, D, scale, (int)V, p0, p1, T, p0 > 0 ? sorted[p0 - 1].x : -1, col, 32,
+        [&](int64_t p) { return sorted[p]; }, [&](const float(&acc)[1]) { *entering = acc[0]; },
+        [&](int id, const float(&acc)[1]) {
+          owner = id;
+          *leaving = acc[0];
+        });
+  __syncthreads();
+  if (owner < 0) return;
+  float* to = dE + (int64_t)owner * D + col;
+  const float before = *to;
+  float acc = *leaving;
+  for (int w = warp + 1; w < kSortWarps; ++w) {
+    const int q0 = begin(w);
+    if (q0 == begin(w + 1)) continue;  // an empty share
+    if (sorted[q0].x != owner) break;
+    acc += part[w * 64 + lane];
+  }
+  *to = fmaf(scale, acc, before);
 }
 
 // Tokens per chunk: enough (chunk, slice) groups to fill the GPU several times
 // over, few enough partial sums (2 rows of D per chunk) to stay small beside
 // the gradient rows.
 int chunk_tokens(int64_t T, int64_t D) {
-  const int64_t groups = 2048;
-  const int64_t slices = row_split(D, kChunkThreads).slices;
-  int chunk = 16;
-  while (chunk < 256 && T * slices > groups * chunk) chunk *= 2;
-  return chunk;
+  const RowSplit r = row_split(D, 4 * kChunkUnits, kChunkThreads);
+  const int64_t groups = std::max<int64_t>(1, kChunkGroups * (kChunkThreads / r.tx) / r.slices);
+  return (int)std::min<int64_t>(256, std::max<int64_t>(8, (T + groups - 1) / groups));
 }
 
 struct EmbedWs {
   int2* buf[2];
+  int* n_runs;
+  int2* runs;     // [n_chunks]
   float* part;
 };
 
@@ -303,41 +671,88 @@ size_t carve_embed(void* ws, int64_t T, int64_t D, EmbedWs* w) {
   };
   const int64_t chunk = chunk_tokens(T, D);
   const size_t o_a = take(8 * (size_t)T), o_b = take(8 * (size_t)T);
-  const size_t o_p = take(8 * (size_t)((T + chunk - 1) / chunk) * (size_t)D);
+  const size_t n_chunks = (size_t)((T + chunk - 1) / chunk);
+  const size_t o_r = take(16 + 8 * n_chunks);
+  const size_t o_p = take(8 * n_chunks * (size_t)D);
   if (w != nullptr) {
     uint8_t* b = static_cast<uint8_t*>(ws);
     w->buf[0] = reinterpret_cast<int2*>(b + o_a);
     w->buf[1] = reinterpret_cast<int2*>(b + o_b);
+    w->n_runs = reinterpret_cast<int*>(b + o_r);
+    w->runs = reinterpret_cast<int2*>(b + o_r + 16);
     w->part = reinterpret_cast<float*>(b + o_p);
   }
   return off;
 }
 
 template <bool kVec, class In>
-cudaError_t launch_sums(const SumArgs& a, dim3 grid, dim3 block, cudaStream_t stream) {
+cudaError_t launch_sums(const SumArgs& a, int n_sm, cudaStream_t stream) {
+  const RowSplit s = row_split(a.D, kVec ? 4 * kChunkUnits : kScalarCols, kChunkThreads);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
+  cfg.blockDim = dim3(s.tx, kChunkThreads / s.tx);
+  cfg.gridDim = dim3((unsigned)((a.n_chunks + cfg.blockDim.y - 1) / cfg.blockDim.y), s.slices);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, embed_chunk_kernel<kVec, In>, a);
-  if (e != cudaSuccess || a.n_chunks == 1) return e;
-  return cudaLaunchKernelEx(&cfg, embed_join_kernel<kVec>, a);
+  cudaError_t e;
+  if constexpr (kVec) {
+    auto kern = embed_chunk_kernel<In, kChunkUnits, kChunkSlots>;
+    cfg.dynamicSmemBytes = (size_t)kChunkSlots * kChunkUnits * (4 * sizeof(In) + 16) * kChunkThreads +
+                           (size_t)cfg.blockDim.y * (2 * a.chunk + 3) * 8;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kern, a);
+  } else {
+    e = cudaLaunchKernelEx(&cfg, embed_chunk_scalar_kernel<In>, a);
+  }
+  if (e != cudaSuccess || a.n_chunks < 3) return e;
+  // (a run with parts enters a whole chunk: at most one per two chunks)
+  const int64_t items = (a.n_chunks / 2) * ((a.D + 127) / 128);
+  return launch_pdl(embed_join_kernel<kVec>, (unsigned)std::min<int64_t>(items, (int64_t)n_sm * 8), kJoinThreads, 0,
+                    stream, a);
 }
 
-template <bool kVec, class In>
-void launch_forward(const int32_t* ids, int64_t T, const void* E, int64_t V, int D, float scale, bool out_bf16,
-                    void* out, unsigned* err, dim3 grid, dim3 block, cudaStream_t stream) {
-  if (out_bf16)
-    embed_forward_kernel<kVec><<<grid, block, 0, stream>>>(ids, T, static_cast<const In*>(E), V, D, scale,
-                                                           static_cast<uint16_t*>(out), err);
-  else
-    embed_forward_kernel<kVec><<<grid, block, 0, stream>>>(ids, T, static_cast<const In*>(E), V, D, scale,
-                                                           static_cast<float*>(out), err);
+template <int kHold>
+cudaError_t launch_sort(const SortArgs& a, cudaStream_t stream) {
+  const int smem = (int)sizeof(SortSmem) + kHold * kSortThreads * (int)sizeof(int2);
+  const cudaError_t e =
+      cudaFuncSetAttribute(embed_sort_kernel<kHold>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaFuncSetAttribute(embed_sort_kernel<kHold>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  embed_sort_kernel<kHold><<<kSortCtas, kSortThreads, smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <class In>
+cudaError_t launch_small(const int32_t* ids, int64_t T, int64_t V, int passes, const void* dout, int D, float scale,
+                         float* dE, unsigned* err, cudaStream_t stream) {
+  const int smem = (int)sizeof(SortSmem) + kSmallTokens * 8 + kSortWarps * 64 * 4;
+  const cudaError_t e = cudaFuncSetAttribute(embed_small_kernel<In>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  embed_small_kernel<In><<<(unsigned)((D + 31) / 32), kSortThreads, smem, stream>>>(
+      ids, (int)T, V, passes, static_cast<const In*>(dout), D, scale, dE, err);
+  return cudaGetLastError();
+}
+
+// Rows per thread: 4 once that leaves a CTA for every SM.
+template <bool kVec, class In, class Out>
+void launch_forward(const int32_t* ids, int64_t T, const void* E, int64_t V, int D, float scale, void* out,
+                    unsigned* err, int n_sm, cudaStream_t stream) {
+  const RowSplit s = row_split(D, 8, kEmbedThreads);
+  const dim3 block(s.tx, kEmbedThreads / s.tx);
+  const bool many = T * s.slices >= (int64_t)n_sm * 4 * block.y;
+  const dim3 grid((unsigned)((T + block.y * (many ? 4 : 1) - 1) / (block.y * (many ? 4 : 1))), s.slices);
+  (many ? embed_forward_kernel<kVec, In, Out, 4> : embed_forward_kernel<kVec, In, Out, 1>)<<<grid, block, 0, stream>>>(
+      ids, T, static_cast<const In*>(E), V, D, scale, static_cast<Out*>(out), err);
+}
+
+template <class In, class Out>
+void forward_rows(bool vec, const int32_t* ids, int64_t T, const void* E, int64_t V, int D, float scale, void* out,
+                  unsigned* err, int n_sm, cudaStream_t stream) {
+  (vec ? launch_forward<true, In, Out> : launch_forward<false, In, Out>)(ids, T, E, V, D, scale, out, err, n_sm,
+                                                                        stream);
 }
 
 }  // namespace
@@ -347,16 +762,13 @@ mole_status embed_forward(const int32_t* ids, int64_t T, const void* E, int64_t 
   unsigned* err = error_word();
   const int n_sm = num_sms();
   if (!err || n_sm <= 0) return MOLE_ERR_CUDA;
-  const bool vec = D % 8 == 0 && aligned16(E) && aligned16(out);
-  const RowSplit s = row_split(D, kEmbedThreads);
-  const dim3 block(s.tx, kEmbedThreads / s.tx);
-  const dim3 grid((unsigned)std::min<int64_t>((T + block.y - 1) / block.y, 1 << 20), s.slices);
+  const bool vec = D % 4 == 0 && aligned_rows(E, E_bf16) && aligned_rows(out, out_bf16);
   if (E_bf16)
-    (vec ? launch_forward<true, uint16_t> : launch_forward<false, uint16_t>)(ids, T, E, V, (int)D, scale, out_bf16, out,
-                                                                            err, grid, block, stream);
+    (out_bf16 ? forward_rows<uint16_t, uint16_t> : forward_rows<uint16_t, float>)(vec, ids, T, E, V, (int)D, scale, out,
+                                                                                 err, n_sm, stream);
   else
-    (vec ? launch_forward<true, float> : launch_forward<false, float>)(ids, T, E, V, (int)D, scale, out_bf16, out, err,
-                                                                      grid, block, stream);
+    (out_bf16 ? forward_rows<float, uint16_t> : forward_rows<float, float>)(vec, ids, T, E, V, (int)D, scale, out, err,
+                                                                           n_sm, stream);
   return cuda_status(cudaGetLastError());
 }
 
@@ -366,24 +778,33 @@ mole_status embed_backward(const int32_t* ids, int64_t T, const void* dout, bool
                            float scale, float* dE, void* ws, cudaStream_t stream) {
   unsigned* err = error_word();
   if (!err) return MOLE_ERR_CUDA;
+  const int n_sm = num_sms();
+  if (n_sm <= 0) return MOLE_ERR_NO_DEVICE;
   EmbedWs w{};
   carve_embed(ws, T, D, &w);
   int bits = 0;  // of the keys 0 .. V
   while (bits < 32 && (V >> bits) != 0) ++bits;
-  SortArgs sa{ids, T, V, {w.buf[0], w.buf[1]}, (bits + 7) / 8, err};
-  embed_sort_kernel<<<kSortCtas, kSortThreads, 0, stream>>>(sa);
-  if (cudaGetLastError() != cudaSuccess) return MOLE_ERR_CUDA;
-  const int chunk = chunk_tokens(T, D);
-  SumArgs a{w.buf[0], T, V, (int)D, chunk, (T + chunk - 1) / chunk, dout, scale, dE, w.part};
-  const RowSplit s = row_split(D, kChunkThreads);
-  const dim3 block(s.tx, kChunkThreads / s.tx);
-  const dim3 grid((unsigned)((a.n_chunks + block.y - 1) / block.y), s.slices);
-  const bool vec = D % 8 == 0 && aligned16(dout) && aligned16(dE);
+  const int passes = (bits + 7) / 8;
+  const bool vec = D % 4 == 0 && aligned_rows(dout, bf16) && aligned16(dE);
   cudaError_t e;
-  if (bf16)
-    e = vec ? launch_sums<true, uint16_t>(a, grid, block, stream) : launch_sums<false, uint16_t>(a, grid, block, stream);
+  if (T <= kSmallTokens)
+    return cuda_status((bf16 ? launch_small<uint16_t> : launch_small<float>)(ids, T, V, passes, dout, (int)D, scale, dE,
+                                                                            err, stream));
+  const SortArgs sa{ids, T, V, w.buf[0], w.buf[1], passes, w.n_runs, err};
+  if (T <= 1 * kSortCtas * kSortThreads)
+    e = launch_sort<1>(sa, stream);
+  else if (T <= 4 * kSortCtas * kSortThreads)
+    e = launch_sort<4>(sa, stream);
   else
-    e = vec ? launch_sums<true, float>(a, grid, block, stream) : launch_sums<false, float>(a, grid, block, stream);
+    e = launch_sort<0>(sa, stream);
+  if (e != cudaSuccess) return MOLE_ERR_CUDA;
+  const int chunk = chunk_tokens(T, D);
+  const SumArgs a{w.buf[0], T, V, (int)D, chunk, (T + chunk - 1) / chunk, dout, scale, dE, w.part, w.n_runs,
+            w.runs};
+  if (bf16)
+    e = vec ? launch_sums<true, uint16_t>(a, n_sm, stream) : launch_sums<false, uint16_t>(a, n_sm, stream);
+  else
+    e = vec ? launch_sums<true, float>(a, n_sm, stream) : launch_sums<false, float>(a, n_sm, stream);
   return cuda_status(e);
 }
 

@@ -73,7 +73,7 @@ struct NormFwd {
 // First column and column step of a thread's unit v of 8 columns.
 template <bool kVec>
 __device__ __forceinline__ int unit_col(int v) {
-  return kVec ? 8 * (v * (int)blockDim.x + (int)threadIdx.x) : v * 8 * (int)blockDim.x + (int)threadIdx.x;
+  return 8 * v * (int)blockDim.x + (kVec ? 4 : 1) * (int)threadIdx.x;
 }
 
 // blockDim = (threads per row, rows per CTA); kUnits units of 8 columns a thread.
@@ -413,7 +413,8 @@ extern "C" mole_status mole_block_norm_forward(const void* x, mole_dtype dt_x, c
   if (st != MOLE_OK) return st;
   const int n_sm = num_sms();
   if (n_sm <= 0) return MOLE_ERR_NO_DEVICE;
-  const bool vec = D % 8 == 0 && aligned16(x) && aligned16(f) && aligned16(x_out) && aligned16(h) &&
+  const bool vec = D % 4 == 0 && aligned_rows(x, dt_x == MOLE_BF16) && aligned_rows(f, dt_f == MOLE_BF16) &&
+                   aligned_rows(x_out, dt_x == MOLE_BF16) && aligned_rows(h, dt_h == MOLE_BF16) &&
                    aligned16(w_post) && aligned16(w_pre);
   const NormFwd a{x, f, w_post, gate, w_pre, res_scale, eps, T, (int)D, x_out, h};
   const RowPlan p = row_plan(D);
@@ -463,8 +464,8 @@ extern "C" mole_status mole_block_norm_backward(const void* x_out, mole_dtype dt
   if (st != MOLE_OK) return st;
   const int n_sm = num_sms();
   if (n_sm <= 0) return MOLE_ERR_NO_DEVICE;
-  const bool vec = D % 8 == 0 && aligned16(x_out) && aligned16(f) && aligned16(w_post) && aligned16(w_pre) &&
-                   aligned16(dx_out) && aligned16(dh) && aligned16(dx) && aligned16(df);
+  const bool vec = D % 4 == 0 && aligned_rows(x_out, dt_x == MOLE_BF16) && aligned_rows(f, dt_f == MOLE_BF16) &&
+                   aligned16(w_post) && aligned16(w_pre) && aligned16(dx_out) && aligned16(dh) && aligned16(dx) && aligned16(df);
   const NormBwd a{x_out, f, w_post, gate, w_pre, res_scale, eps, T, (int)D, dx_out, dh, dx, df, dgate, part_post, part_pre};
   const RowPlan p = row_plan(D);
   const bool xb = dt_x == MOLE_BF16, fb = dt_f == MOLE_BF16;

@@ -44,39 +44,131 @@ __device__ __forceinline__ void st_vec8(uint16_t* p, const float (&f)[8]) {
       make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
 }
 
-// A thread's 8 columns of a row: consecutive (kVec; col0 = 8 * thread), or
-// spaced by `step` from col0 = thread, those past D left out.
-template <bool kVec, class T>
-__device__ __forceinline__ void ld_cols(const T* row, int col0, int step, int D, float (&f)[8]) {
+// How a group of `step` threads holds the columns of a row, C a thread: with
+// vector accesses (kVec: D a multiple of 4, rows aligned to 4 elements) in
+// units of 4 columns, unit u of thread i at 4 (i + u step), so that every access
+// of a warp is contiguous; else column k of thread i at i + k step.  `col0` is
+// the thread's first column, and what lies at or past D is left out.
+
+// Loads of a unit of 4 columns, and their values.
+__device__ __forceinline__ void ld_unit(const float* p, float (&f)[4]) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+}
+__device__ __forceinline__ void ld_unit(const uint16_t* p, float (&f)[4]) {
+  const uint2 a = *reinterpret_cast<const uint2*>(p);
+  f[0] = bf16_lo(a.x); f[1] = bf16_hi(a.x); f[2] = bf16_lo(a.y); f[3] = bf16_hi(a.y);
+}
+__device__ __forceinline__ void st_unit(float* p, float a, float b, float c, float d) {
+  *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
+}
+__device__ __forceinline__ void st_unit(uint16_t* p, float a, float b, float c, float d) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(a, b), pack_bf16(c, d));
+}
+
+template <bool kVec, int C, class T>
+__device__ __forceinline__ void ld_cols(const T* row, int col0, int step, int D, float (&f)[C]) {
   if constexpr (kVec) {
-    ld_vec8(row + col0, f);
+#pragma unroll
+    for (int u = 0; u < C / 4; ++u) {
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+      if (col0 + 4 * u * step < D) ld_unit(row + col0 + 4 * u * step, x);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[4 * u + k] = x[k];
+    }
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = col0 + k * step < D ? ld1(row + col0 + k * step) : 0.f;
+    for (int k = 0; k < C; ++k) f[k] = col0 + k * step < D ? ld1(row + col0 + k * step) : 0.f;
   }
 }
-template <bool kVec, class T>
-__device__ __forceinline__ void st_cols(T* row, int col0, int step, int D, const float (&f)[8]) {
+template <bool kVec, int C, class T>
+__device__ __forceinline__ void st_cols(T* row, int col0, int step, int D, const float (&f)[C]) {
   if constexpr (kVec) {
-    st_vec8(row + col0, f);
+#pragma unroll
+    for (int u = 0; u < C / 4; ++u)
+      if (col0 + 4 * u * step < D)
+        st_unit(row + col0 + 4 * u * step, f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3]);
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
+    for (int k = 0; k < C; ++k)
       if (col0 + k * step < D) st1(row + col0 + k * step, f[k]);
   }
 }
 
-// How a row of D columns is spread: groups of tx threads, each thread 8
+// A thread's C columns of a row as loaded (converted when they are used, so
+// that a load in flight holds no more registers than its bytes).
+template <bool kVec, class T, int C>
+struct RowUnit {
+  static constexpr int kWords = (C * (int)sizeof(T) + 3) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* row, int col0, int step, int D) {
+    if constexpr (kVec) {
+#pragma unroll
+      for (int u = 0; u < C / 4; ++u) {
+        if (col0 + 4 * u * step >= D) continue;
+        if constexpr (sizeof(T) == 4) {
+          const uint4 x = *reinterpret_cast<const uint4*>(row + col0 + 4 * u * step);
+          w[4 * u] = x.x; w[4 * u + 1] = x.y; w[4 * u + 2] = x.z; w[4 * u + 3] = x.w;
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(row + col0 + 4 * u * step);
+          w[2 * u] = x.x; w[2 * u + 1] = x.y;
+        }
+      }
+    } else {
+      uint32_t x[C];
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        const int c = col0 + k * step;
+        if constexpr (sizeof(T) == 4)
+          x[k] = c < D ? __float_as_uint(row[c]) : 0u;
+        else
+          x[k] = c < D ? (uint32_t)row[c] : 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < kWords; ++i)
+        w[i] = sizeof(T) == 4 ? x[i] : 2 * i + 1 < C ? x[2 * i] | (x[(2 * i + 1) % C] << 16) : x[2 * i];
+    }
+  }
+  __device__ __forceinline__ void get(float (&f)[C]) const {
+#pragma unroll
+    for (int k = 0; k < C; ++k) {
+      if constexpr (sizeof(T) == 4)
+        f[k] = __uint_as_float(w[k]);
+      else
+        f[k] = k & 1 ? bf16_hi(w[k / 2]) : bf16_lo(w[k / 2]);
+    }
+  }
+};
+
+// Asynchronous copies (8 or 16 bytes) into shared memory, in groups of the
+// thread's own.
+template <int kBytes>
+__device__ __forceinline__ void cp_async(void* smem, const void* global) {
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(global) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(smem)), "l"(global) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+// How a row of D columns is spread: groups of tx threads, each thread `unit`
 // columns, `slices` groups side by side.
 struct RowSplit {
   int tx, slices;
 };
-RowSplit row_split(int64_t D, int max_tx) {
-  const int64_t units = (D + 7) / 8;
+RowSplit row_split(int64_t D, int unit, int max_tx) {
+  const int64_t units = (D + unit - 1) / unit;
   int tx = 1;
   while (tx < max_tx && tx < units) tx *= 2;
   return {tx, (int)((units + tx - 1) / tx)};
 }
+
+// Whether vector accesses (units of 4 columns) can start at p.
+bool aligned_rows(const void* p, bool bf16) { return bf16 ? aligned8(p) : aligned16(p); }
 
 // Pointers aligned to n bytes (a power of two).
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

@@ -39,7 +39,7 @@ def _check_forward(mole, x, f, w_post, gate, res_scale, w_pre, th, in_place=Fals
 
 
 @pytest.mark.parametrize("tx,tf,th", [(F32, F32, BF16), (BF16, BF16, BF16), (F32, BF16, F32), (BF16, F32, F32)])
-@pytest.mark.parametrize("T,D", [(1, 1), (1, 2048), (3, 7), (9, 64), (130, 256), (65, 264), (37, 1001), (20, 2056),
+@pytest.mark.parametrize("T,D", [(1, 1), (1, 2048), (3, 7), (9, 64), (10, 20), (130, 256), (65, 264), (37, 1001), (20, 2056),
                                  (11, 4097), (6, 8192), (2000, 128)])
 def test_forward(mole, T, D, tx, tf, th):
     rng = np.random.default_rng(T + D)
@@ -116,7 +116,7 @@ def _check_backward(mole, x, f, w_post, gate, res_scale, w_pre, dx_out, dh, alia
 
 
 @pytest.mark.parametrize("tx,tf", [(F32, F32), (BF16, BF16), (F32, BF16), (BF16, F32)])
-@pytest.mark.parametrize("T,D", [(1, 1), (1, 2048), (3, 7), (9, 64), (130, 256), (65, 264), (37, 1001), (20, 2056),
+@pytest.mark.parametrize("T,D", [(1, 1), (1, 2048), (3, 7), (9, 64), (10, 20), (130, 256), (65, 264), (37, 1001), (20, 2056),
                                  (11, 4097), (6, 8192), (3000, 128), (5001, 72)])
 def test_backward(mole, T, D, tx, tf):
     rng = np.random.default_rng(T + D)

@@ -30,7 +30,7 @@ def _check_forward(mole, rng, T, V, D, tin, tout, ids=None, scale=3.7):
 
 @pytest.mark.parametrize("tin", [F32, BF16])
 @pytest.mark.parametrize("tout", [F32, BF16])
-@pytest.mark.parametrize("T,V,D", [(1, 1, 1), (1, 50304, 2048), (7, 3, 8), (33, 100, 1001), (300, 50, 72),
+@pytest.mark.parametrize("T,V,D", [(1, 1, 1), (1, 50304, 2048), (7, 3, 8), (19, 40, 20), (33, 100, 1001), (300, 50, 72),
                                    (513, 1000, 2056), (5, 9, 4099)])
 def test_forward(mole, T, V, D, tin, tout):
     _check_forward(mole, np.random.default_rng(T + D), T, V, D, tin, tout)
@@ -95,6 +95,7 @@ def _check_backward(mole, rng, T, V, D, dtype, ids, scale=1.3, dout=None):
     (1, 1, 1, "uniform"), (1, 50304, 64, "zipf"), (2, 1, 24, "uniform"),   # a key of one bit, one token
     (31, 5, 40, "uniform"), (257, 300, 1001, "zipf"),                      # odd width: scalar columns
     (1000, 40, 512, "uniform"),                                           # every run crosses chunks
+    (2500, 900, 20, "zipf"), (2300, 30, 1001, "zipf"),                  # units of 4 columns; odd width
     (3001, 70000, 136, "zipf"),                                           # three digits of key
     (5000, 300, 2056, "zipf"), (9999, 2, 72, "uniform"),
     (20000, 50304, 256, "zipf"),
@@ -104,7 +105,7 @@ def test_backward(mole, T, V, D, kind, dtype):
     _check_backward(mole, rng, T, V, D, dtype, inputs.draw_ids(rng, T, V, kind))
 
 
-@pytest.mark.parametrize("T", [1, 15, 16, 17, 32, 33, 4096, 40000])
+@pytest.mark.parametrize("T", [1, 15, 16, 17, 32, 33, 2048, 2049, 4096, 40000])
 def test_backward_one_id(mole, T):
     # all tokens one id: a single run over every chunk
     rng = np.random.default_rng(T)

@@ -179,6 +179,11 @@ def test_binding_refusals(mole):
     with pytest.raises(ValueError, match="lengths"):
         mole.mole_adamw_step([w, w], [w], [w, w], [w, w])
     mole.mole_adamw_step([], [], [], [])
+    codes = torch.zeros(8, dtype=torch.float8_e4m3fn)
+    with pytest.raises(ValueError, match="scales"):
+        mole.mole_adamw_step([w], [w], [codes], [codes])
+    with pytest.raises(ValueError, match="scales"):
+        mole.mole_adamw_step([w], [w], [w], [w], m_scales=[w], v_scales=[w])
 
 
 def _differences(f, x, eps=1e-5):
