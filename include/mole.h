@@ -476,9 +476,9 @@ mole_status mole_block_norm_backward(const void* x_out, mole_dtype dt_x, const v
  *
  * tensors and config are HOST structs, read before the call returns.  No
  * memory that a call writes may overlap anything else in its list
- * (MOLE_ERR_ARG).  Any n >= 0 and pointers aligned to their element; 16-byte
- * aligned pointers (8-byte for codes) take the vector path.  One launch per
- * 64 tensors.
+ * (MOLE_ERR_ARG).  Any n >= 0 and pointers aligned to their element; a
+ * tensor whose pointers are all aligned to 4 elements takes vector accesses.  One launch per
+ * 128 tensors.
  */
 typedef struct {
   void* param;         /* [n] dt_param, overwritten */

@@ -4,19 +4,22 @@
 //
 // Elementwise, so bound by HBM: per element the gradient (4 or 2 bytes), the
 // weight (bf16 with an fp32 master: 10 bytes moved, fp32: 8, bf16 alone: 4) and
-// the states (fp32: 16, 8 bits: 4 + 16 / 128).  One launch serves up to 64
+// the states (fp32: 16, 8 bits: 4 + 16 / 128).  One launch serves up to 128
 // tensors: their addresses travel in the kernel's parameters, and the work is
-// cut into chunks of kChunk elements, each inside one tensor.
+// cut into chunks of kAdamChunk elements, each inside one tensor.
 //
-// 8-bit states: a block of 128 consecutive elements is 16 lanes of 8 elements,
-// so its largest value takes four shuffles.  m and sqrt(v) are e4m3 times an
-// fp32 scale; keeping the root halves the exponents that the codes must span.
-// The update of a block reads codes and writes codes; in between everything is
-// fp32.  m, v and the quantiser use separately rounded products and sums (no
-// contraction): which code an element gets then depends on its inputs alone.
+// A thread has kAdamUnits units of 4 elements, so that a warp's unit is 128
+// consecutive ones: every access is contiguous, and it is one block of 8-bit
+// states, whose largest value takes one warp reduction (of the bits: values
+// that are not negative order like their bits, NaN above all).  m and sqrt(v)
+// are e4m3 times an fp32 scale; keeping the root halves the exponents that the
+// codes must span.  In between everything is fp32.  m, v and the quantiser use
+// separately rounded products and sums (no contraction): which code an element
+// gets then depends on its inputs alone.
 #include <cuda_fp8.h>
 
 #include <cmath>
+#include <type_traits>
 #include <vector>
 
 #include "rows.cuh"
@@ -25,10 +28,10 @@ namespace mole {
 namespace {
 
 constexpr int kAdamThreads = 256;
-constexpr int kAdamUnit = 8;                          // elements a thread
-constexpr int kAdamChunk = kAdamThreads * kAdamUnit;  // elements a CTA
+constexpr int kAdamUnits = 2;                               // units of 4 elements a thread
+constexpr int kAdamChunk = 4 * kAdamUnits * kAdamThreads;  // elements a CTA
 constexpr int kAdamBlock = 128;                       // elements per scale
-constexpr int kAdamTensors = 64;                      // per launch
+constexpr int kAdamTensors = 128;                         // per launch (10 KB of parameters)
 constexpr float kInvE4m3Max = (float)(1.0 / 448.0);
 constexpr float kScaleFloor = 0x1p-120f;              // its reciprocal is finite
 constexpr float kE4m3Tiny = 0x1p-9f;                  // the smallest nonzero code
@@ -75,175 +78,211 @@ __host__ __device__ inline void step_factors(double lr, double beta1, double bet
   *root = (float)(1.0 / sqrt(1.0 - int_pow(beta2, t)));
 }
 
-// Elements [0, cnt) of the thread's 8 (cnt = 8 unless the tensor ends here).
-template <class T>
-__device__ __forceinline__ void load_unit(const T* p, int cnt, bool vec, float (&f)[8]) {
-  if (vec && cnt == 8) {
-    ld_vec8(p, f);
+// The unit's elements [0, cnt): all 4 with vector accesses (kFull), or one by
+// one (a tensor's last elements, tensors of other alignment).
+template <bool kFull, class T>
+__device__ __forceinline__ void load_unit(const T* p, int cnt, float (&f)[4]) {
+  if constexpr (kFull) {
+    ld_unit(p, f);
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = k < cnt ? ld1(p + k) : 0.f;
+    for (int k = 0; k < 4; ++k) f[k] = k < cnt ? ld1(p + k) : 0.f;
   }
 }
-template <class T>
-__device__ __forceinline__ void store_unit(T* p, int cnt, bool vec, const float (&f)[8]) {
-  if (vec && cnt == 8) {
-    st_vec8(p, f);
+template <bool kFull, class T>
+__device__ __forceinline__ void store_unit(T* p, int cnt, const float (&f)[4]) {
+  if constexpr (kFull) {
+    st_unit(p, f[0], f[1], f[2], f[3]);
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
+    for (int k = 0; k < 4; ++k)
       if (k < cnt) st1(p + k, f[k]);
   }
 }
 
-__device__ __forceinline__ float2 e4m3_pair(uint16_t c) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c, __NV_E4M3);
-  return __half22float2(__half2(h));
+// Four e4m3 codes.
+template <bool kFull>
+__device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int cnt) {
+  if constexpr (kFull) return *reinterpret_cast<const uint32_t*>(p);
+  uint32_t w = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (k < cnt) w |= (uint32_t)p[k] << (8 * k);
+  return w;
 }
-
-__device__ __forceinline__ void load_codes(const uint8_t* p, int cnt, bool vec, float (&f)[8]) {
-  uint32_t w[2] = {0, 0};
-  if (vec && cnt == 8) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    w[0] = u.x;
-    w[1] = u.y;
+template <bool kFull>
+__device__ __forceinline__ void store_codes(uint8_t* p, int cnt, uint32_t w) {
+  if constexpr (kFull) {
+    *reinterpret_cast<uint32_t*>(p) = w;
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < cnt) w[k >> 2] |= (uint32_t)p[k] << (8 * (k & 3));
+    for (int k = 0; k < 4; ++k)
+      if (k < cnt) p[k] = (uint8_t)(w >> (8 * k));
   }
+}
+__device__ __forceinline__ void decode(uint32_t w, float (&f)[4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 x = e4m3_pair((uint16_t)(w[i >> 1] >> (16 * (i & 1))));
+  for (int i = 0; i < 2; ++i) {
+    const float2 x = __half22float2(
+        __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * i)), __NV_E4M3)));
     f[2 * i] = x.x;
     f[2 * i + 1] = x.y;
   }
 }
-__device__ __forceinline__ void store_codes(uint8_t* p, int cnt, bool vec, const float (&f)[8]) {
-  uint32_t w[2] = {0, 0};
+__device__ __forceinline__ uint32_t encode(const float (&f)[4]) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[0], f[1]), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[2], f[3]), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+// The scale of a block whose largest magnitude has these bits (a NaN stays one).
+__device__ __forceinline__ float block_scale(unsigned bits) {
+  const float s = __fmul_rn(__uint_as_float(__reduce_max_sync(0xffffffffu, bits)), kInvE4m3Max);
+  return s < kScaleFloor ? kScaleFloor : s;
+}
+
+// The tensor of chunk c: the last one whose first chunk is not behind it.
+__device__ __forceinline__ int tensor_of(const AdamArgs& a, unsigned c) {
+  int n = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t c = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i], f[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-    w[i >> 1] |= c << (16 * (i & 1));
+  for (int i = 0; i < kAdamTensors; i += 32) {
+    const int j = i + (threadIdx.x & 31);
+    n += __popc(__ballot_sync(0xffffffffu, j < a.n_tensors && a.first[j] <= c));
   }
-  if (vec && cnt == 8) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-  } else {
+  return n - 1;
+}
+
+// The step's factors: lr, lr / (1 - b1^t), 1 / sqrt(1 - b2^t), the gradients' one.
+struct Factors {
+  float lr, step_size, root, grad;
+};
+
+// The thread's units of a chunk whose first element it has is e0.  kFull: the
+// whole chunk lies in the tensor, with vector accesses; its types are template
+// parameters then (tests per unit made the 8-bit kernel issue-bound: 89
+// instructions an element, 71 now; 619 -> 549 us for 185 M elements).
+template <bool kState8, bool kFull, bool kGradBf16, bool kParamBf16, bool kMaster>
+__device__ __forceinline__ void step_chunk(const AdamArgs& a, const AdamTensor& t, const Factors& w, int64_t e0) {
+  using G = std::conditional_t<kGradBf16, uint16_t, float>;
+  using P = std::conditional_t<kParamBf16, uint16_t, float>;
+  float g[kAdamUnits][4], p[kAdamUnits][4], m[kAdamUnits][4], v[kAdamUnits][4];
+  uint32_t mc[kAdamUnits], vc[kAdamUnits];
+  float sm[kAdamUnits], sv[kAdamUnits];
+  int cnt[kAdamUnits];
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < cnt) p[k] = (uint8_t)(w[k >> 2] >> (8 * (k & 3)));
+  for (int u = 0; u < kAdamUnits; ++u) {
+    const int64_t e = e0 + 4 * u * kAdamThreads;
+    cnt[u] = kFull ? 4 : (int)std::min<int64_t>(4, std::max<int64_t>(0, t.n - e));
+    load_unit<kFull>(static_cast<const G*>(t.grad) + e, cnt[u], g[u]);
+    if constexpr (kMaster)
+      load_unit<kFull>(t.master + e, cnt[u], p[u]);
+    else
+      load_unit<kFull>(static_cast<const P*>(t.param) + e, cnt[u], p[u]);
+    if constexpr (kState8) {
+      mc[u] = load_codes<kFull>(static_cast<const uint8_t*>(t.m) + e, cnt[u]);
+      vc[u] = load_codes<kFull>(static_cast<const uint8_t*>(t.v) + e, cnt[u]);
+      sm[u] = cnt[u] > 0 ? t.m_scale[e / kAdamBlock] : 0.f;
+      sv[u] = cnt[u] > 0 ? t.v_scale[e / kAdamBlock] : 0.f;
+    } else {
+      load_unit<kFull>(static_cast<const float*>(t.m) + e, cnt[u], m[u]);
+      load_unit<kFull>(static_cast<const float*>(t.v) + e, cnt[u], v[u]);
+    }
+  }
+  const float decay = w.lr * t.weight_decay;
+#pragma unroll
+  for (int u = 0; u < kAdamUnits; ++u) {
+    const int64_t e = e0 + 4 * u * kAdamThreads;
+    float r[4];
+    unsigned m_max = 0, r_max = 0;
+    if constexpr (kState8) {
+      decode(mc[u], m[u]);
+      decode(vc[u], v[u]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (kState8) {
+        m[u][k] = __fmul_rn(m[u][k], sm[u]);
+        v[u][k] = __fmul_rn(v[u][k], sv[u]);
+        v[u][k] = __fmul_rn(v[u][k], v[u][k]);
+      }
+      g[u][k] *= w.grad;
+      m[u][k] = __fadd_rn(__fmul_rn(m[u][k], a.b1), __fmul_rn(g[u][k], a.omb1));
+      v[u][k] = __fadd_rn(__fmul_rn(v[u][k], a.b2), __fmul_rn(__fmul_rn(g[u][k], g[u][k]), a.omb2));
+      r[k] = __fsqrt_rn(v[u][k]);
+      const float step = __fdividef(m[u][k], fmaf(r[k], w.root, a.eps));
+      p[u][k] = fmaf(-w.step_size, step, fmaf(-decay, p[u][k], p[u][k]));
+      if constexpr (kState8) {
+        m_max = max(m_max, __float_as_uint(fabsf(m[u][k])));
+        r_max = max(r_max, __float_as_uint(r[k]));
+      }
+    }
+    if constexpr (kMaster) store_unit<kFull>(t.master + e, cnt[u], p[u]);
+    store_unit<kFull>(static_cast<P*>(t.param) + e, cnt[u], p[u]);
+    if constexpr (kState8) {
+      const float nm = block_scale(m_max), nv = block_scale(r_max);
+      const float im = __frcp_rn(nm), iv = __frcp_rn(nv);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        m[u][k] = __fmul_rn(m[u][k], im);
+        const float q = __fmul_rn(r[k], iv);
+        v[u][k] = r[k] > 0.f && q < kE4m3Tiny ? kE4m3Tiny : q;
+      }
+      store_codes<kFull>(static_cast<uint8_t*>(t.m) + e, cnt[u], encode(m[u]));
+      store_codes<kFull>(static_cast<uint8_t*>(t.v) + e, cnt[u], encode(v[u]));
+      if (cnt[u] > 0 && (threadIdx.x & 31) == 0) {
+        t.m_scale[e / kAdamBlock] = nm;
+        t.v_scale[e / kAdamBlock] = nv;
+      }
+    } else {
+      store_unit<kFull>(static_cast<float*>(t.m) + e, cnt[u], m[u]);
+      store_unit<kFull>(static_cast<float*>(t.v) + e, cnt[u], v[u]);
+    }
   }
 }
 
-// The largest of a block's values (16 lanes; NaN where one is NaN).
-__device__ __forceinline__ float block_max(float v) {
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
-    const float u = __shfl_xor_sync(0xffffffffu, v, o);
-    v = (u > v || u != u) ? u : v;
+template <bool kState8, bool kFull>
+__device__ __forceinline__ void step_types(const AdamArgs& a, const AdamTensor& t, const Factors& w, int64_t e0) {
+  if (t.grad_bf16) {
+    if (t.master)
+      step_chunk<kState8, kFull, true, true, true>(a, t, w, e0);
+    else if (t.param_bf16)
+      step_chunk<kState8, kFull, true, true, false>(a, t, w, e0);
+    else
+      step_chunk<kState8, kFull, true, false, false>(a, t, w, e0);
+  } else {
+    if (t.master)
+      step_chunk<kState8, kFull, false, true, true>(a, t, w, e0);
+    else if (t.param_bf16)
+      step_chunk<kState8, kFull, false, true, false>(a, t, w, e0);
+    else
+      step_chunk<kState8, kFull, false, false, false>(a, t, w, e0);
   }
-  return v;
 }
 
 template <bool kState8>
-__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamArgs a) {
+__global__ void __launch_bounds__(kAdamThreads, 4) adamw_kernel(const __grid_constant__ AdamArgs a) {
   __shared__ float factors[3];
-  if (threadIdx.x == 0) {
-    float lr = a.lr, step_size = a.step_size, root = a.root;
-    if (a.step_dev || a.lr_dev) {
+  Factors w{a.lr, a.step_size, a.root, a.grad_scale ? *a.grad_scale : 1.f};
+  if (a.step_dev || a.lr_dev) {
+    if (threadIdx.x == 0) {
       const double l = a.lr_dev ? (double)*a.lr_dev : a.lr_host;
-      lr = (float)l;
-      step_factors(l, a.beta1, a.beta2, a.step_dev ? *a.step_dev : a.step, &step_size, &root);
+      factors[0] = (float)l;
+      step_factors(l, a.beta1, a.beta2, a.step_dev ? *a.step_dev : a.step, &factors[1], &factors[2]);
     }
-    factors[0] = lr;
-    factors[1] = step_size;
-    factors[2] = root;
+    __syncthreads();
+    w.lr = factors[0];
+    w.step_size = factors[1];
+    w.root = factors[2];
   }
-  __syncthreads();
-  const float lr = factors[0], step_size = factors[1], root = factors[2];
-  const float gs = a.grad_scale ? *a.grad_scale : 1.f;
   const unsigned total = a.first[a.n_tensors];
   for (unsigned c = blockIdx.x; c < total; c += gridDim.x) {
-    int i = 0, end = a.n_tensors;  // the tensor i with first[i] <= c < first[i + 1]
-    while (end - i > 1) {
-      const int mid = (i + end) >> 1;
-      if (a.first[mid] <= c)
-        i = mid;
-      else
-        end = mid;
-    }
+    const int i = tensor_of(a, c);
     const AdamTensor& t = a.t[i];
-    const int64_t e0 = (int64_t)(c - a.first[i]) * kAdamChunk + kAdamUnit * threadIdx.x;
-    const int cnt = (int)std::min<int64_t>(kAdamUnit, std::max<int64_t>(0, t.n - e0));
-    const bool vec = t.vec != 0;
-    float g[8], p[8], m[8], v[8];
-    if (t.grad_bf16)
-      load_unit(static_cast<const uint16_t*>(t.grad) + e0, cnt, vec, g);
+    const int64_t start = (int64_t)(c - a.first[i]) * kAdamChunk;
+    if (t.vec && start + kAdamChunk <= t.n)
+      step_types<kState8, true>(a, t, w, start + 4 * threadIdx.x);
     else
-      load_unit(static_cast<const float*>(t.grad) + e0, cnt, vec, g);
-    if (t.master)
-      load_unit(t.master + e0, cnt, vec, p);
-    else if (t.param_bf16)
-      load_unit(static_cast<const uint16_t*>(t.param) + e0, cnt, vec, p);
-    else
-      load_unit(static_cast<const float*>(t.param) + e0, cnt, vec, p);
-    const int64_t block = e0 / kAdamBlock;
-    if constexpr (kState8) {
-      load_codes(static_cast<const uint8_t*>(t.m) + e0, cnt, vec, m);
-      load_codes(static_cast<const uint8_t*>(t.v) + e0, cnt, vec, v);
-      const float sm = cnt > 0 ? t.m_scale[block] : 0.f, sv = cnt > 0 ? t.v_scale[block] : 0.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        m[k] = __fmul_rn(m[k], sm);
-        v[k] = __fmul_rn(v[k], sv);
-        v[k] = __fmul_rn(v[k], v[k]);
-      }
-    } else {
-      load_unit(static_cast<const float*>(t.m) + e0, cnt, vec, m);
-      load_unit(static_cast<const float*>(t.v) + e0, cnt, vec, v);
-    }
-    const float decay = lr * t.weight_decay;
-    float m_max = 0.f, r_max = 0.f;
-    float r[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      g[k] *= gs;
-      m[k] = __fadd_rn(__fmul_rn(m[k], a.b1), __fmul_rn(g[k], a.omb1));
-      v[k] = __fadd_rn(__fmul_rn(v[k], a.b2), __fmul_rn(__fmul_rn(g[k], g[k]), a.omb2));
-      r[k] = __fsqrt_rn(v[k]);
-      p[k] = p[k] - p[k] * decay - step_size * (m[k] / fmaf(r[k], root, a.eps));
-      if constexpr (kState8) {
-        const float am = fabsf(m[k]);
-        m_max = (am > m_max || am != am) ? am : m_max;
-        r_max = (r[k] > r_max || r[k] != r[k]) ? r[k] : r_max;
-      }
-    }
-    if (t.master) store_unit(t.master + e0, cnt, vec, p);
-    if (t.param_bf16)
-      store_unit(static_cast<uint16_t*>(t.param) + e0, cnt, vec, p);
-    else
-      store_unit(static_cast<float*>(t.param) + e0, cnt, vec, p);
-    if constexpr (kState8) {
-      m_max = __fmul_rn(block_max(m_max), kInvE4m3Max);
-      r_max = __fmul_rn(block_max(r_max), kInvE4m3Max);
-      const float sm = m_max < kScaleFloor ? kScaleFloor : m_max, sv = r_max < kScaleFloor ? kScaleFloor : r_max;
-      const float im = __frcp_rn(sm), iv = __frcp_rn(sv);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        m[k] = __fmul_rn(m[k], im);
-        const float q = __fmul_rn(r[k], iv);
-        v[k] = r[k] > 0.f && q < kE4m3Tiny ? kE4m3Tiny : q;
-      }
-      store_codes(static_cast<uint8_t*>(t.m) + e0, cnt, vec, m);
-      store_codes(static_cast<uint8_t*>(t.v) + e0, cnt, vec, v);
-      if (cnt > 0 && (threadIdx.x & 15) == 0) {
-        t.m_scale[block] = sm;
-        t.v_scale[block] = sv;
-      }
-    } else {
-      store_unit(static_cast<float*>(t.m) + e0, cnt, vec, m);
-      store_unit(static_cast<float*>(t.v) + e0, cnt, vec, v);
-    }
+      step_types<kState8, false>(a, t, w, start + 4 * threadIdx.x);
   }
 }
 
@@ -322,7 +361,7 @@ mole_status run_adamw(const mole_adamw_tensor* tensors, int32_t n_tensors, const
   a.lr_dev = c->lr_dev;
   a.grad_scale = c->grad_scale_dev;
   if (!c->step_dev && !c->lr_dev) step_factors(c->lr, c->beta1, c->beta2, c->step, &a.step_size, &a.root);
-  const size_t state_align = c->state8 ? 8 : 16;
+  const size_t state_align = c->state8 ? 4 : 16;  // of a unit's 4 elements
   auto launch = [&]() -> mole_status {
     if (a.n_tensors == 0) return MOLE_OK;
     const unsigned grid = std::min<unsigned>(a.first[a.n_tensors], (unsigned)n_sm * 256u);
@@ -344,8 +383,8 @@ mole_status run_adamw(const mole_adamw_tensor* tensors, int32_t n_tensors, const
     AdamTensor& d = a.t[a.n_tensors];
     d = {t.param, t.grad, t.master, t.m, t.v, t.m_scale, t.v_scale, t.n, t.weight_decay, t.dt_param == MOLE_BF16,
          t.dt_grad == MOLE_BF16,
-         aligned16(t.param) && aligned16(t.grad) && aligned16(t.master) && aligned_to(t.m, state_align) &&
-             aligned_to(t.v, state_align)};
+         aligned_rows(t.param, t.dt_param == MOLE_BF16) && aligned_rows(t.grad, t.dt_grad == MOLE_BF16) &&
+             aligned16(t.master) && aligned_to(t.m, state_align) && aligned_to(t.v, state_align)};
     a.first[a.n_tensors + 1] = a.first[a.n_tensors] + (unsigned)chunks;
     ++a.n_tensors;
   }

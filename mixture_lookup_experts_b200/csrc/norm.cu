@@ -3,9 +3,9 @@
 // layer's router and shared expert read the previous layer's output; what lies
 // between two blocks' GEMMs is one pass over the token rows:
 //     y = w_post f / rms(f),  x' = beta x + gate y,  h = w_pre x' / rms(x')
-// A token's row is held in registers, 8 columns a thread, by a group of one to
-// 16 warps; the row's sums are reduced by shuffles and (beyond one warp) shared
-// memory.  Each tensor is read and written once: both kernels are bound by HBM.
+// A token's row is held in registers, 8 columns a thread, by a CTA of one to
+// 16 warps; the row's sums are reduced by shuffles and (beyond one warp) shared memory.
+// Each tensor is read and written once: both kernels are bound by HBM.
 //
 // Backward, per token (n = D, r = 1/rms):
 //     G  = dx' + r_x (a - x^ <a, x^>/n)      a = dh w_pre,  x^ = x' r_x
@@ -22,11 +22,10 @@
 namespace mole {
 namespace {
 
-constexpr int kMaxRowThreads = 512;   // leaves 128 registers a thread
-constexpr int kNormThreads = 256;     // CTA size while a row needs no more
-constexpr int64_t kMaxNormD = 2 * 8 * kMaxRowThreads;
-constexpr int kMaxNormCtas = 1024;    // rows of partial sums in the workspace
-constexpr int kReduceCols = 32, kReduceRows = 32;
+constexpr int kRowThreads = 256, kMaxRowThreads = 512;  // a row's threads, up to 4096 columns and beyond
+constexpr int64_t kMaxNormD = 16 * kMaxRowThreads;
+constexpr int kStages = 2;
+constexpr int kReduceUnits = 8, kReduceRows = 128;  // 32 columns and 32 warps a CTA
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -34,27 +33,70 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sums of K values over a row's group of threads (blockDim.x, a multiple of
-// 32), in a fixed order.  `red` holds K floats per warp of the CTA and serves
-// one call between two barriers of the row loop.
+// Sums of K <= 4 values over the CTA's threads (a multiple of 32), in a fixed
+// order.  `red` holds a float4 per warp of the CTA (K == 1: a
+// float); a call that reuses it comes at least one other call (one barrier)
+// later.
 template <int K>
-__device__ __forceinline__ void row_sums(float (&v)[K], float* red) {
+__device__ __forceinline__ void row_sums(float (&v)[K], float4* red) {
 #pragma unroll
   for (int k = 0; k < K; ++k) v[k] = warp_sum(v[k]);
   const int warps = blockDim.x >> 5;
   if (warps == 1) return;
   const int warp = threadIdx.x >> 5;
-  float* mine = red + (size_t)threadIdx.y * warps * K;
-  if ((threadIdx.x & 31) == 0) {
+  if constexpr (K == 1) {
+    // (what pads the warps to a multiple of 4 is left out of the sum)
+    const int quads = (warps + 3) >> 2;
+    if ((threadIdx.x & 31) == 0) reinterpret_cast<float*>(red)[warp] = v[0];
+    __syncthreads();
+    float sum = 0.f;
+    for (int q = 0; q < quads; ++q) {
+      const float4 x = red[q];
+      sum += x.x;
+      if (4 * q + 1 < warps) sum += x.y;
+      if (4 * q + 2 < warps) sum += x.z;
+      if (4 * q + 3 < warps) sum += x.w;
+    }
+    v[0] = sum;
+  } else {
+    if ((threadIdx.x & 31) == 0)
+      red[warp] = make_float4(v[0], v[1], K > 2 ? v[K > 2 ? 2 : 0] : 0.f, K > 3 ? v[K > 3 ? 3 : 0] : 0.f);
+    __syncthreads();
+    float4 sum = red[0];
+    for (int w = 1; w < warps; ++w) {
+      const float4 x = red[w];
+      sum.x += x.x; sum.y += x.y; sum.z += x.z; sum.w += x.w;
+    }
+    const float out[4] = {sum.x, sum.y, sum.z, sum.w};
 #pragma unroll
-    for (int k = 0; k < K; ++k) mine[warp * K + k] = v[k];
+    for (int k = 0; k < K; ++k) v[k] = out[k];
   }
-  __syncthreads();
+}
+
+// A thread's columns of a row on their way through shared memory (cp.async;
+// each thread reads back its own copies only).  at: the thread's place in the
+// stage's area of this tensor, which lies there as in the row.  kFull: the
+// threads' columns are exactly the row's.
+template <bool kFull, int C, class T>
+__device__ __forceinline__ void stage_put(uint8_t* at, const T* row, int col0, int step, int D) {
 #pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = 0.f;
-  for (int w = 0; w < warps; ++w)
+  for (int u = 0; u < C / 4; ++u)
+    if (kFull || col0 + 4 * u * step < D) cp_async<4 * sizeof(T)>(at + u * step * 4 * sizeof(T), row + 4 * u * step);
+}
+template <bool kFull, int C, class T>
+__device__ __forceinline__ void stage_get(const uint8_t* at, int col0, int step, int D, float (&f)[C]) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] += mine[w * K + k];
+  for (int u = 0; u < C / 4; ++u) {
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    if (kFull || col0 + 4 * u * step < D) ld_unit(reinterpret_cast<const T*>(at + u * step * 4 * sizeof(T)), x);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f[4 * u + k] = x[k];
+  }
+}
+
+template <bool kVec, bool kFull, int C>
+__device__ __forceinline__ void ld_weights(const float* w, int col0, int step, int D, float (&f)[C]) {
+  ld_cols<kVec, C, float, kVec && kFull>(w, col0, step, D, f);
 }
 
 struct NormFwd {
@@ -70,85 +112,83 @@ struct NormFwd {
   void* h;
 };
 
-// First column and column step of a thread's unit v of 8 columns.
-template <bool kVec>
-__device__ __forceinline__ int unit_col(int v) {
-  return 8 * v * (int)blockDim.x + (kVec ? 4 : 1) * (int)threadIdx.x;
-}
-
-// blockDim = (threads per row, rows per CTA); kUnits units of 8 columns a thread.
-template <bool kVec, int kUnits, class X, class F, class H>
-__global__ void __launch_bounds__(kMaxRowThreads) norm_forward_kernel(const NormFwd a) {
-  __shared__ float red[2][kMaxRowThreads / 32];
+// A CTA has a row at a time, C columns a thread.  kStages > 0:
+// rows come through shared memory, kStages - 1 of them ahead of the one in work
+// (loads of a row then overlap the sums and stores of the one before);
+// kStages == 0: straight into registers.
+template <bool kVec, int C, int kStages, int kThreads, class X, class F, class H>
+__global__ void __launch_bounds__(kThreads) norm_forward_kernel(const NormFwd a) {
+  __shared__ float4 red[2][2][kMaxRowThreads / 32];
+  extern __shared__ __align__(16) uint8_t norm_smem[];
   const int step = blockDim.x, D = a.D;
+  const int c0 = (kVec ? 4 : 1) * (int)threadIdx.x;
   const float inv_d = 1.f / (float)D;
-  for (int64_t t0 = (int64_t)blockIdx.x * blockDim.y; t0 < a.T; t0 += (int64_t)gridDim.x * blockDim.y) {
-    const int64_t t = t0 + threadIdx.y;
-    const bool in = t < a.T;
-    float x[kUnits][8], f[kUnits][8];
-    float s[1] = {0.f};
-    const X* xr = static_cast<const X*>(a.x) + t * D;
-    const F* fr = static_cast<const F*>(a.f) + t * D;
-#pragma unroll
-    for (int v = 0; v < kUnits; ++v) {
-      const int c = unit_col<kVec>(v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) x[v][k] = f[v][k] = 0.f;
-      if (in && c < D) {
-        ld_cols<kVec>(xr, c, step, D, x[v]);
-        if (a.f) ld_cols<kVec>(fr, c, step, D, f[v]);
-      }
+  const X* x_in = static_cast<const X*>(a.x);
+  const F* f_in = static_cast<const F*>(a.f);
+  const int stage_bytes = step * C * (int)(sizeof(X) + sizeof(F));
+  const int x_at = c0 * (int)sizeof(X), f_at = step * C * (int)sizeof(X) + c0 * (int)sizeof(F);
+  const int64_t stride = gridDim.x;
+  int64_t t = blockIdx.x;
+  auto fetch = [&](int64_t row, int stage) {
+    if (row < a.T) {
+      uint8_t* at = norm_smem + stage * stage_bytes;
+      stage_put<false, C>(at + x_at, x_in + row * D + c0, c0, step, D);
+      if (f_in) stage_put<false, C>(at + f_at, f_in + row * D + c0, c0, step, D);
     }
-    float g = 1.f;
-    if (a.f) {
-      if (a.gate && in) g = a.gate[t];
+    cp_async_commit();
+  };
+  if constexpr (kStages > 0) {
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) fetch(t + k * stride, k);
+  }
+  int stage = 0, parity = 0;
+  for (; t < a.T; t += stride, parity ^= 1) {
+    float x[C], f[C];
+    float s[1] = {0.f};
+    if constexpr (kStages > 0) {
+      fetch(t + (kStages - 1) * stride, stage == 0 ? kStages - 1 : stage - 1);
+      cp_async_wait<kStages - 1>();
+      const uint8_t* at = norm_smem + stage * stage_bytes;
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+      stage_get<false, C, X>(at + x_at, c0, step, D, x);
+      if (f_in) stage_get<false, C, F>(at + f_at, c0, step, D, f);
+    } else {
+      ld_cols<kVec>(x_in + t * D, c0, step, D, x);
+      if (f_in) ld_cols<kVec>(f_in + t * D, c0, step, D, f);
+    }
+    if (f_in) {
+      const float g = a.gate ? a.gate[t] : 1.f;
       if (a.w_post) {
+        float w[C];
+        ld_cols<kVec>(a.w_post, c0, step, D, w);
 #pragma unroll
-        for (int v = 0; v < kUnits; ++v)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) s[0] = fmaf(f[v][k], f[v][k], s[0]);
-        row_sums(s, red[0]);
+        for (int k = 0; k < C; ++k) s[0] = fmaf(f[k], f[k], s[0]);
+        row_sums(s, red[parity][0]);
         const float r = rsqrtf(fmaf(s[0], inv_d, a.eps));
 #pragma unroll
-        for (int v = 0; v < kUnits; ++v) {
-          const int c = unit_col<kVec>(v);
-          float w[8];
-          if (c < D) {
-            ld_cols<kVec>(a.w_post, c, step, D, w);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) f[v][k] = f[v][k] * r * w[k];
-          }
-        }
+        for (int k = 0; k < C; ++k) f[k] = f[k] * r * w[k];
       }
-    }
-    s[0] = 0.f;
 #pragma unroll
-    for (int v = 0; v < kUnits; ++v) {
-      const int c = unit_col<kVec>(v);
+      for (int k = 0; k < C; ++k) x[k] = fmaf(g, f[k], a.res_scale * x[k]);
+    } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        x[v][k] = a.f ? fmaf(g, f[v][k], a.res_scale * x[v][k]) : a.res_scale * x[v][k];
-        s[0] = fmaf(x[v][k], x[v][k], s[0]);
-      }
-      if (in && a.x_out && c < D) st_cols<kVec>(static_cast<X*>(a.x_out) + t * D, c, step, D, x[v]);
+      for (int k = 0; k < C; ++k) x[k] *= a.res_scale;
     }
+    if (a.x_out) st_cols<kVec>(static_cast<X*>(a.x_out) + t * D, c0, step, D, x);
     if (a.h) {
-      row_sums(s, red[1]);
+      float w[C];
+      ld_cols<kVec>(a.w_pre, c0, step, D, w);
+      s[0] = 0.f;
+#pragma unroll
+      for (int k = 0; k < C; ++k) s[0] = fmaf(x[k], x[k], s[0]);
+      row_sums(s, red[parity][1]);
       const float r = rsqrtf(fmaf(s[0], inv_d, a.eps));
 #pragma unroll
-      for (int v = 0; v < kUnits; ++v) {
-        const int c = unit_col<kVec>(v);
-        if (in && c < D) {
-          float w[8];
-          ld_cols<kVec>(a.w_pre, c, step, D, w);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) w[k] *= x[v][k] * r;
-          st_cols<kVec>(static_cast<H*>(a.h) + t * D, c, step, D, w);
-        }
-      }
+      for (int k = 0; k < C; ++k) w[k] *= x[k] * r;
+      st_cols<kVec>(static_cast<H*>(a.h) + t * D, c0, step, D, w);
     }
-    if (blockDim.x > 32) __syncthreads();  // red's readers are done
   }
+  if constexpr (kStages > 0) cp_async_wait<0>();
 }
 
 struct NormBwd {
@@ -165,233 +205,272 @@ struct NormBwd {
   float* dx;
   float* df;
   float* dgate;
-  float* part_post;  // [gridDim.x][D] or null
+  float* part_post;  // [gridDim.x][D rounded up to 4] or null
   float* part_pre;
 };
 
-template <bool kVec, int kUnits, class X, class F>
-__global__ void __launch_bounds__(kMaxRowThreads) norm_backward_kernel(const NormBwd a) {
-  __shared__ float red[2][3 * (kMaxRowThreads / 32)];
-  extern __shared__ float fold[];  // several rows per CTA: their sums before one is written
+// kFull: every input but the gate is there, dx and df are wanted, and the
+// threads' columns are exactly the row's (no tests per column: backward of
+// 16384 x 2048 168 -> 130 us).
+template <bool kVec, bool kFull, int C, int kStages, int kThreads, class X, class F>
+__global__ void __launch_bounds__(kThreads) norm_backward_kernel(const NormBwd a) {
+  __shared__ float4 red[2][2][kMaxRowThreads / 32];
+  extern __shared__ __align__(16) uint8_t norm_smem[];
+  pdl_trigger();  // norm_reduce_kernel may take its place
   const int step = blockDim.x, D = a.D;
+  const int c0 = (kVec ? 4 : 1) * (int)threadIdx.x;
   const float inv_d = 1.f / (float)D;
-  float acc_pre[kUnits][8], acc_post[kUnits][8];
+  const bool has_h = kFull || a.dh, has_xo = kFull || a.dx_out, has_f = kFull || a.f, post = kFull || a.w_post;
+  const X* x_in = static_cast<const X*>(a.x);
+  const F* f_in = static_cast<const F*>(a.f);
+  // a stage: dh, dx_out, x, f
+  const int h_at = 4 * c0, g_at = step * C * 4 + 4 * c0, x_at = step * C * 8 + c0 * (int)sizeof(X),
+            f_at = step * C * (8 + (int)sizeof(X)) + c0 * (int)sizeof(F),
+            stage_bytes = step * C * (8 + (int)(sizeof(X) + sizeof(F)));
+  const int64_t stride = gridDim.x;
+  int64_t t = blockIdx.x;
+  auto fetch = [&](int64_t row, int stage) {
+    if (row < a.T) {
+      uint8_t* at = norm_smem + stage * stage_bytes;
+      const int64_t off = row * D + c0;
+      if (has_h) {
+        stage_put<kFull, C>(at + h_at, a.dh + off, c0, step, D);
+        stage_put<kFull, C>(at + x_at, x_in + off, c0, step, D);
+      }
+      if (has_xo) stage_put<kFull, C>(at + g_at, a.dx_out + off, c0, step, D);
+      if (has_f) stage_put<kFull, C>(at + f_at, f_in + off, c0, step, D);
+    }
+    cp_async_commit();
+  };
+  if constexpr (kStages > 0) {
 #pragma unroll
-  for (int v = 0; v < kUnits; ++v)
+    for (int k = 0; k < kStages - 1; ++k) fetch(t + k * stride, k);
+  }
+  float acc_pre[C], acc_post[C];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) acc_pre[v][k] = acc_post[v][k] = 0.f;
-  for (int64_t t0 = (int64_t)blockIdx.x * blockDim.y; t0 < a.T; t0 += (int64_t)gridDim.x * blockDim.y) {
-    const int64_t t = t0 + threadIdx.y;
-    const bool in = t < a.T;
-    float x[kUnits][8], f[kUnits][8], dh[kUnits][8], G[kUnits][8];
+  for (int k = 0; k < C; ++k) acc_pre[k] = acc_post[k] = 0.f;
+  int stage = 0, parity = 0;
+  for (; t < a.T; t += stride, parity ^= 1) {
+    float x[C], f[C], dh[C], G[C];
+    if constexpr (!kFull) {
+#pragma unroll
+      for (int k = 0; k < C; ++k) x[k] = f[k] = dh[k] = G[k] = 0.f;
+    }
+    if constexpr (kStages > 0) {
+      fetch(t + (kStages - 1) * stride, stage == 0 ? kStages - 1 : stage - 1);
+      cp_async_wait<kStages - 1>();
+      const uint8_t* at = norm_smem + stage * stage_bytes;
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+      if (has_h) {
+        stage_get<kFull, C, float>(at + h_at, c0, step, D, dh);
+        stage_get<kFull, C, X>(at + x_at, c0, step, D, x);
+      }
+      if (has_xo) stage_get<kFull, C, float>(at + g_at, c0, step, D, G);
+      if (has_f) stage_get<kFull, C, F>(at + f_at, c0, step, D, f);
+    } else {
+      if (has_h) {
+        ld_cols<kVec>(a.dh + t * D, c0, step, D, dh);
+        ld_cols<kVec>(x_in + t * D, c0, step, D, x);
+      }
+      if (has_xo) ld_cols<kVec>(a.dx_out + t * D, c0, step, D, G);
+      if (has_f) ld_cols<kVec>(f_in + t * D, c0, step, D, f);
+    }
+    const float g = a.gate ? a.gate[t] : 1.f;
+    float w[C];
     float s[3] = {0.f, 0.f, 0.f};
+    if (has_h) {
+      ld_weights<kVec, kFull>(a.w_pre, c0, step, D, w);
 #pragma unroll
-    for (int v = 0; v < kUnits; ++v) {
-      const int c = unit_col<kVec>(v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) x[v][k] = f[v][k] = dh[v][k] = G[v][k] = 0.f;
-      if (in && c < D) {
-        if (a.dh) {
-          ld_cols<kVec>(static_cast<const X*>(a.x) + t * D, c, step, D, x[v]);
-          ld_cols<kVec>(a.dh + t * D, c, step, D, dh[v]);
-        }
-        if (a.f) ld_cols<kVec>(static_cast<const F*>(a.f) + t * D, c, step, D, f[v]);
-        if (a.dx_out) ld_cols<kVec>(a.dx_out + t * D, c, step, D, G[v]);
+      for (int k = 0; k < C; ++k) {
+        s[0] = fmaf(x[k], x[k], s[0]);
+        w[k] *= dh[k];
+        s[1] = fmaf(w[k], x[k], s[1]);
       }
     }
-    const float g = a.gate && in ? a.gate[t] : 1.f;
 #pragma unroll
-    for (int v = 0; v < kUnits; ++v) {
-      const int c = unit_col<kVec>(v);
-      float w[8];
-      if (a.dh && c < D) {
-        ld_cols<kVec>(a.w_pre, c, step, D, w);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          s[0] = fmaf(x[v][k], x[v][k], s[0]);
-          s[1] = fmaf(dh[v][k] * w[k], x[v][k], s[1]);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) s[2] = fmaf(f[v][k], f[v][k], s[2]);
-    }
-    row_sums(s, red[0]);
-    const float rf = a.w_post ? rsqrtf(fmaf(s[2], inv_d, a.eps)) : 1.f;
-    float q[1] = {0.f};
-    if (a.dh) {
+    for (int k = 0; k < C; ++k) s[2] = fmaf(f[k], f[k], s[2]);
+    row_sums(s, red[parity][0]);
+    const float rf = post ? rsqrtf(fmaf(s[2], inv_d, a.eps)) : 1.f;
+    if (has_h) {
       const float rx = rsqrtf(fmaf(s[0], inv_d, a.eps));
       const float cx = rx * rx * (s[1] * inv_d);  // <a, x^> / n = rx s1 / n; x^ = rx x'
 #pragma unroll
-      for (int v = 0; v < kUnits; ++v) {
-        const int c = unit_col<kVec>(v);
-        if (c < D) {
-          float w[8];
-          ld_cols<kVec>(a.w_pre, c, step, D, w);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            acc_pre[v][k] = fmaf(dh[v][k], x[v][k] * rx, acc_pre[v][k]);
-            G[v][k] += rx * fmaf(-cx, x[v][k], dh[v][k] * w[k]);
-          }
-        }
+      for (int k = 0; k < C; ++k) {
+        acc_pre[k] = fmaf(dh[k], x[k] * rx, acc_pre[k]);
+        G[k] = fmaf(rx, fmaf(-cx, x[k], w[k]), G[k]);
       }
     }
-    // f becomes f^ (f itself without a post-norm); dh becomes dy w_post / gate = G w_post
+    // f becomes f^ (f itself without a post-norm); dh becomes G w_post
+    if (post) {
+      ld_weights<kVec, kFull>(a.w_post, c0, step, D, w);
+    } else {
 #pragma unroll
-    for (int v = 0; v < kUnits; ++v) {
-      const int c = unit_col<kVec>(v);
-      float w[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) w[k] = 1.f;
-      if (a.w_post && c < D) ld_cols<kVec>(a.w_post, c, step, D, w);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        f[v][k] *= rf;
-        acc_post[v][k] = fmaf(g * G[v][k], f[v][k], acc_post[v][k]);
-        dh[v][k] = G[v][k] * w[k];
-        q[0] = fmaf(dh[v][k], f[v][k], q[0]);
-      }
-      if (in && a.dx && c < D) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) G[v][k] *= a.res_scale;
-        st_cols<kVec>(a.dx + t * D, c, step, D, G[v]);
-      }
+      for (int k = 0; k < C; ++k) w[k] = 1.f;
     }
-    if (a.f) {
-      row_sums(q, red[1]);
-      if (in && a.dgate && threadIdx.x == 0) a.dgate[t] = q[0];
+    float q[1] = {0.f};
+#pragma unroll
+    for (int k = 0; k < C; ++k) {
+      f[k] *= rf;
+      acc_post[k] = fmaf(g * G[k], f[k], acc_post[k]);
+      dh[k] = G[k] * w[k];
+      q[0] = fmaf(dh[k], f[k], q[0]);
     }
-    if (a.df && in) {
-      const float cf = a.w_post ? q[0] * inv_d : 0.f;
+    if (kFull || a.dx) {
 #pragma unroll
-      for (int v = 0; v < kUnits; ++v) {
-        const int c = unit_col<kVec>(v);
-        if (c < D) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) dh[v][k] = g * rf * fmaf(-cf, f[v][k], dh[v][k]);
-          st_cols<kVec>(a.df + t * D, c, step, D, dh[v]);
-        }
-      }
+      for (int k = 0; k < C; ++k) G[k] *= a.res_scale;
+      st_cols<kVec, C, float, kFull>(a.dx + t * D, c0, step, D, G);
     }
-    if (blockDim.x > 32) __syncthreads();  // red's readers are done
-  }
-  // the CTA's sums over its rows: group by group into one row of the workspace
-  for (int which = 0; which < 2; ++which) {
-    float* part = which ? a.part_post : a.part_pre;
-    if (!part) continue;
-    for (int r = 0; r < (int)blockDim.y; ++r) {
-      if ((int)threadIdx.y == r) {
+    if (has_f) {
+      row_sums(q, red[parity][1]);
+      if (a.dgate && threadIdx.x == 0) a.dgate[t] = q[0];
+    }
+    if (kFull || a.df) {
+      const float cf = post ? -(q[0] * inv_d) : 0.f, gr = g * rf;
 #pragma unroll
-        for (int v = 0; v < kUnits; ++v) {
-          const int c = unit_col<kVec>(v);
-          if (c >= D) continue;
-          float w[8];
-          if (r > 0) {
-            ld_cols<kVec>(fold, c, step, D, w);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) w[k] += which ? acc_post[v][k] : acc_pre[v][k];
-          } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) w[k] = which ? acc_post[v][k] : acc_pre[v][k];
-          }
-          if (r == (int)blockDim.y - 1)
-            st_cols<kVec>(part + (int64_t)blockIdx.x * D, c, step, D, w);
-          else
-            st_cols<kVec>(fold, c, step, D, w);
-        }
-      }
-      if (blockDim.y > 1) __syncthreads();
+      for (int k = 0; k < C; ++k) dh[k] = gr * fmaf(cf, f[k], dh[k]);
+      st_cols<kVec, C, float, kFull>(a.df + t * D, c0, step, D, dh);
     }
   }
+  if constexpr (kStages > 0) cp_async_wait<0>();
+  if (a.part_pre) st_cols<kVec>(a.part_pre + (int64_t)blockIdx.x * ((D + 3) & ~3), c0, step, D, acc_pre);
+  if (a.part_post) st_cols<kVec>(a.part_post + (int64_t)blockIdx.x * ((D + 3) & ~3), c0, step, D, acc_post);
 }
 
-// dw[d] += sum over the CTAs' rows, in order: a thread takes every
-// kReduceRows-th row of its column, then the 32 sums are added in order.
-// blockIdx.y: 0 = dw_pre, 1 = dw_post.
-__global__ void __launch_bounds__(kReduceCols* kReduceRows)
-    norm_reduce_kernel(const float* part_pre, const float* part_post, int rows, int D, float* dw_pre, float* dw_post) {
-  __shared__ float s[kReduceRows][kReduceCols + 1];
-  pdl_wait();
+// dw[d] += sum over the CTAs' rows, in a fixed order: 4 columns a thread, 128
+// rows side by side, then 32 sums per column from shared memory.  blockIdx.y:
+// 0 = dw_pre, 1 = dw_post.  Rows are `ld` floats apart (a multiple of 4).
+__global__ void __launch_bounds__(kReduceUnits* kReduceRows)
+    norm_reduce_kernel(const float* part_pre, const float* part_post, int rows, int D, int ld, float* dw_pre,
+                       float* dw_post) {
+  constexpr int kCols = 4 * kReduceUnits;
+  __shared__ float s[kCols][kCols + 1];  // [warp][column]
   const float* part = blockIdx.y ? part_post : part_pre;
   float* dw = blockIdx.y ? dw_post : dw_pre;
   if (!part) return;
-  const int d = blockIdx.x * kReduceCols + threadIdx.x;
-  float acc = 0.f;
-  if (d < D)
-    for (int r = threadIdx.y; r < rows; r += kReduceRows) acc += part[(int64_t)r * D + d];
-  s[threadIdx.y][threadIdx.x] = acc;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int unit = lane & (kReduceUnits - 1), row = threadIdx.x / kReduceUnits;
+  const int d = blockIdx.x * kCols + 4 * unit;
+  pdl_wait();
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  if (d < D) {
+#pragma unroll 4
+    for (int r = row; r < rows; r += kReduceRows) {
+      const float4 x = *reinterpret_cast<const float4*>(part + (int64_t)r * ld + d);
+      acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+#pragma unroll
+    for (int o = kReduceUnits; o < 32; o *= 2) acc[k] += __shfl_xor_sync(0xffffffffu, acc[k], o);
+    if (lane < kReduceUnits) s[warp][4 * lane + k] = acc[k];
+  }
   __syncthreads();
-  if (threadIdx.y == 0 && d < D) {
-    float sum = 0.f;
-    for (int r = 0; r < kReduceRows; ++r) sum += s[r][threadIdx.x];
-    dw[d] += sum;
+  const float sum = warp_sum(s[lane][warp]);  // warp = column
+  if (lane == 0 && blockIdx.x * kCols + warp < D) dw[blockIdx.x * kCols + warp] += sum;
+}
+
+// The kernels' forms, by columns per thread.  Vector rows: staged, 8 columns
+// while a warp has a row's worth and 16 beyond (the sums over the threads then
+// cost half the instructions per column: forward of 16384 x 2048 78.7 -> 76.2
+// us), up to 4096 columns, where two rows of the widest types fit shared
+// memory; beyond, straight into registers.  Rows of other widths or alignment:
+// 4 columns a thread (their loads are single elements: more threads), 16 where
+// 512 threads of 4 are not enough.
+enum class Form { kStaged8, kStaged16, kVector, kScalar, kScalarWide };
+Form row_form(bool vec, int64_t D) {
+  if (!vec) return D <= 4 * kMaxRowThreads ? Form::kScalar : Form::kScalarWide;
+  return D <= 256 ? Form::kStaged8 : D <= 16 * kRowThreads ? Form::kStaged16 : Form::kVector;
+}
+
+// A row's threads: a multiple of 32.
+int row_threads(int64_t D, int cols) { return (int)(((D + cols - 1) / cols + 31) / 32 * 32); }
+
+// The backward's CTAs, each with a row of partial sums: up to 1024 threads on
+// each of 148 SMs, and no more than 16 CTAs there.
+int64_t max_backward_ctas(int threads) { return 148 * std::min(16, 1024 / threads); }
+
+// CTAs of a persistent launch: as many as fit the GPU at once.
+template <class K>
+cudaError_t resident_ctas(K kern, int threads, size_t smem, int n_sm, int64_t most, unsigned* grid) {
+  *grid = (unsigned)std::min<int64_t>(most, n_sm);
+  cudaError_t e = cudaSuccess;
+  if (smem > 40 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (most <= n_sm || e != cudaSuccess) return e;
+  int occ = 0;
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, threads, smem);
+  if (e == cudaSuccess && occ < 1) e = cudaErrorInvalidConfiguration;
+  *grid = (unsigned)std::min<int64_t>(most, (int64_t)n_sm * occ);
+  return e;
+}
+
+template <bool kVec, int C, int kStages, int kThreads, class X, class F, class H>
+cudaError_t forward_launch(const NormFwd& a, int n_sm, cudaStream_t stream) {
+  auto kern = norm_forward_kernel<kVec, C, kStages, kThreads, X, F, H>;
+  const int threads = row_threads(a.D, C);
+  const size_t smem = (size_t)kStages * threads * C * (sizeof(X) + sizeof(F));
+  unsigned grid = 0;
+  const cudaError_t e = resident_ctas(kern, threads, smem, n_sm, a.T, &grid);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, threads, smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <class X, class F, class H>
+cudaError_t forward_form(const NormFwd& a, Form form, int n_sm, cudaStream_t stream) {
+  switch (form) {
+    case Form::kStaged8: return forward_launch<true, 8, kStages, kRowThreads, X, F, H>(a, n_sm, stream);
+    case Form::kStaged16: return forward_launch<true, 16, kStages, kRowThreads, X, F, H>(a, n_sm, stream);
+    case Form::kVector: return forward_launch<true, 16, 0, kMaxRowThreads, X, F, H>(a, n_sm, stream);
+    case Form::kScalar: return forward_launch<false, 4, 0, kMaxRowThreads, X, F, H>(a, n_sm, stream);
+    default: return forward_launch<false, 16, 0, kMaxRowThreads, X, F, H>(a, n_sm, stream);
   }
 }
 
-// How rows are spread over a CTA: threads per row (a multiple of 32), rows per
-// CTA, units of 8 columns per thread.
-struct RowPlan {
-  int tx, rows, units;
-};
-RowPlan row_plan(int64_t D) {
-  const int units = D > 8 * kMaxRowThreads ? 2 : 1;
-  const int64_t threads = (D + 8 * units - 1) / (8 * units);
-  const int tx = (int)((threads + 31) / 32 * 32);
-  return {tx, std::max(1, kNormThreads / tx), units};
+template <class X>
+cudaError_t forward_types(const NormFwd& a, bool f_bf16, bool h_bf16, Form form, int n_sm, cudaStream_t stream) {
+  if (f_bf16)
+    return h_bf16 ? forward_form<X, uint16_t, uint16_t>(a, form, n_sm, stream)
+                  : forward_form<X, uint16_t, float>(a, form, n_sm, stream);
+  return h_bf16 ? forward_form<X, float, uint16_t>(a, form, n_sm, stream)
+                : forward_form<X, float, float>(a, form, n_sm, stream);
 }
 
-template <bool kVec, int kUnits, class X, class F, class H>
-cudaError_t forward_launch(const NormFwd& a, const RowPlan& p, int n_sm, cudaStream_t stream) {
-  const int64_t ctas = (a.T + p.rows - 1) / p.rows;
-  const unsigned grid = (unsigned)std::min<int64_t>(ctas, (int64_t)n_sm * 8);
-  norm_forward_kernel<kVec, kUnits, X, F, H><<<grid, dim3(p.tx, p.rows), 0, stream>>>(a);
+template <bool kVec, bool kFull, int C, int kStages, int kThreads, class X, class F>
+cudaError_t backward_launch(const NormBwd& a, int n_sm, int* ctas, cudaStream_t stream) {
+  auto kern = norm_backward_kernel<kVec, kFull, C, kStages, kThreads, X, F>;
+  const int threads = row_threads(a.D, C);
+  const size_t smem = (size_t)kStages * threads * C * (8 + sizeof(X) + sizeof(F));
+  unsigned grid = 0;
+  const cudaError_t e = resident_ctas(kern, threads, smem, n_sm, std::min<int64_t>(a.T, max_backward_ctas(threads)), &grid);
+  if (e != cudaSuccess) return e;
+  *ctas = (int)grid;
+  kern<<<grid, threads, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
-template <bool kVec, int kUnits, class X, class F>
-cudaError_t forward_h(const NormFwd& a, bool h_bf16, const RowPlan& p, int n_sm, cudaStream_t stream) {
-  return h_bf16 ? forward_launch<kVec, kUnits, X, F, uint16_t>(a, p, n_sm, stream)
-                : forward_launch<kVec, kUnits, X, F, float>(a, p, n_sm, stream);
-}
-
-template <bool kVec, int kUnits>
-cudaError_t forward_xf(const NormFwd& a, bool x_bf16, bool f_bf16, bool h_bf16, const RowPlan& p, int n_sm,
-                       cudaStream_t stream) {
-  if (x_bf16)
-    return f_bf16 ? forward_h<kVec, kUnits, uint16_t, uint16_t>(a, h_bf16, p, n_sm, stream)
-                  : forward_h<kVec, kUnits, uint16_t, float>(a, h_bf16, p, n_sm, stream);
-  return f_bf16 ? forward_h<kVec, kUnits, float, uint16_t>(a, h_bf16, p, n_sm, stream)
-                : forward_h<kVec, kUnits, float, float>(a, h_bf16, p, n_sm, stream);
-}
-
-int backward_ctas(int64_t T, const RowPlan& p, int n_sm) {
-  return (int)std::min<int64_t>((T + p.rows - 1) / p.rows, std::min(kMaxNormCtas, n_sm * 4));
-}
-
-template <bool kVec, int kUnits, class X, class F>
-cudaError_t backward_launch(const NormBwd& a, const RowPlan& p, int n_sm, cudaStream_t stream) {
-  const int grid = backward_ctas(a.T, p, n_sm);
-  const size_t smem = p.rows > 1 ? (size_t)a.D * 4 : 0;
-  norm_backward_kernel<kVec, kUnits, X, F><<<grid, dim3(p.tx, p.rows), smem, stream>>>(a);
-  return cudaGetLastError();
-}
-
-template <bool kVec, int kUnits>
-cudaError_t backward_xf(const NormBwd& a, bool x_bf16, bool f_bf16, const RowPlan& p, int n_sm, cudaStream_t stream) {
-  if (x_bf16)
-    return f_bf16 ? backward_launch<kVec, kUnits, uint16_t, uint16_t>(a, p, n_sm, stream)
-                  : backward_launch<kVec, kUnits, uint16_t, float>(a, p, n_sm, stream);
-  return f_bf16 ? backward_launch<kVec, kUnits, float, uint16_t>(a, p, n_sm, stream)
-                : backward_launch<kVec, kUnits, float, float>(a, p, n_sm, stream);
+template <class X, class F>
+cudaError_t backward_form(const NormBwd& a, Form form, int n_sm, int* ctas, cudaStream_t stream) {
+  const bool full = a.dh && a.dx_out && a.f && a.w_post && a.dx && a.df && a.D % (16 * 32) == 0;
+  switch (form) {
+    case Form::kStaged8: return backward_launch<true, false, 8, kStages, kRowThreads, X, F>(a, n_sm, ctas, stream);
+    case Form::kStaged16:
+      return full ? backward_launch<true, true, 16, kStages, kRowThreads, X, F>(a, n_sm, ctas, stream)
+                  : backward_launch<true, false, 16, kStages, kRowThreads, X, F>(a, n_sm, ctas, stream);
+    case Form::kVector: return backward_launch<true, false, 16, 0, kMaxRowThreads, X, F>(a, n_sm, ctas, stream);
+    case Form::kScalar: return backward_launch<false, false, 4, 0, kMaxRowThreads, X, F>(a, n_sm, ctas, stream);
+    default: return backward_launch<false, false, 16, 0, kMaxRowThreads, X, F>(a, n_sm, ctas, stream);
+  }
 }
 
 bool valid(mole_dtype dt) { return dt == MOLE_F32 || dt == MOLE_BF16; }
 size_t size_of(mole_dtype dt) { return dt == MOLE_BF16 ? 2 : 4; }
 
-// Rows of partial sums of each weight gradient.
+// Rows of partial sums of each weight gradient, 16-byte aligned.
+int64_t part_ld(int64_t D) { return (D + 3) / 4 * 4; }
 size_t partial_bytes(int64_t T, int64_t D) {
-  const RowPlan p = row_plan(D);
-  const size_t rows = (size_t)std::min<int64_t>((T + p.rows - 1) / p.rows, kMaxNormCtas);
-  return (rows * (size_t)D * 4 + 255) / 256 * 256;
+  const int64_t rows = std::min<int64_t>(T, max_backward_ctas(row_threads(D, 16)));  // 16: the fewest threads
+  return ((size_t)rows * (size_t)part_ld(D) * 4 + 255) / 256 * 256;
 }
 
 }  // namespace
@@ -417,14 +496,10 @@ extern "C" mole_status mole_block_norm_forward(const void* x, mole_dtype dt_x, c
                    aligned_rows(x_out, dt_x == MOLE_BF16) && aligned_rows(h, dt_h == MOLE_BF16) &&
                    aligned16(w_post) && aligned16(w_pre);
   const NormFwd a{x, f, w_post, gate, w_pre, res_scale, eps, T, (int)D, x_out, h};
-  const RowPlan p = row_plan(D);
-  const bool xb = dt_x == MOLE_BF16, fb = dt_f == MOLE_BF16, hb = dt_h == MOLE_BF16;
-  cudaError_t e;
-  if (p.units == 1)
-    e = vec ? forward_xf<true, 1>(a, xb, fb, hb, p, n_sm, stream) : forward_xf<false, 1>(a, xb, fb, hb, p, n_sm, stream);
-  else
-    e = vec ? forward_xf<true, 2>(a, xb, fb, hb, p, n_sm, stream) : forward_xf<false, 2>(a, xb, fb, hb, p, n_sm, stream);
-  return cuda_status(e);
+  const Form form = row_form(vec, D);
+  const bool fb = dt_f == MOLE_BF16, hb = dt_h == MOLE_BF16;
+  return cuda_status(dt_x == MOLE_BF16 ? forward_types<uint16_t>(a, fb, hb, form, n_sm, stream)
+                                       : forward_types<float>(a, fb, hb, form, n_sm, stream));
 }
 
 extern "C" size_t mole_block_norm_backward_workspace(int64_t T, int64_t D) {
@@ -467,18 +542,29 @@ extern "C" mole_status mole_block_norm_backward(const void* x_out, mole_dtype dt
   const bool vec = D % 4 == 0 && aligned_rows(x_out, dt_x == MOLE_BF16) && aligned_rows(f, dt_f == MOLE_BF16) &&
                    aligned16(w_post) && aligned16(w_pre) && aligned16(dx_out) && aligned16(dh) && aligned16(dx) && aligned16(df);
   const NormBwd a{x_out, f, w_post, gate, w_pre, res_scale, eps, T, (int)D, dx_out, dh, dx, df, dgate, part_post, part_pre};
-  const RowPlan p = row_plan(D);
-  const bool xb = dt_x == MOLE_BF16, fb = dt_f == MOLE_BF16;
+  const Form form = row_form(vec, D);
+  int ctas = 0;
   cudaError_t e;
-  if (p.units == 1)
-    e = vec ? backward_xf<true, 1>(a, xb, fb, p, n_sm, stream) : backward_xf<false, 1>(a, xb, fb, p, n_sm, stream);
+  if (dt_x == MOLE_BF16)
+    e = dt_f == MOLE_BF16 ? backward_form<uint16_t, uint16_t>(a, form, n_sm, &ctas, stream)
+                          : backward_form<uint16_t, float>(a, form, n_sm, &ctas, stream);
   else
-    e = vec ? backward_xf<true, 2>(a, xb, fb, p, n_sm, stream) : backward_xf<false, 2>(a, xb, fb, p, n_sm, stream);
+    e = dt_f == MOLE_BF16 ? backward_form<float, uint16_t>(a, form, n_sm, &ctas, stream)
+                          : backward_form<float, float>(a, form, n_sm, &ctas, stream);
   if (e != cudaSuccess) return MOLE_ERR_CUDA;
   if (part_pre || part_post) {
-    norm_reduce_kernel<<<dim3((unsigned)((D + kReduceCols - 1) / kReduceCols), 2), dim3(kReduceCols, kReduceRows), 0,
-                         stream>>>(part_pre, part_post, backward_ctas(T, p, n_sm), (int)D, dw_pre, dw_post);
-    if (cudaGetLastError() != cudaSuccess) return MOLE_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((D + 4 * kReduceUnits - 1) / (4 * kReduceUnits)), 2);
+    cfg.blockDim = dim3(kReduceUnits * kReduceRows);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, norm_reduce_kernel, (const float*)part_pre, (const float*)part_post, ctas, (int)D,
+                           (int)part_ld(D), dw_pre, dw_post) != cudaSuccess)
+      return MOLE_ERR_CUDA;
   }
   return MOLE_OK;
 }

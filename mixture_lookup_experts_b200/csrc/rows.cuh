@@ -21,29 +21,10 @@ __device__ __forceinline__ float ld1<uint16_t>(const uint16_t* p) {
 __device__ __forceinline__ void st1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void st1(uint16_t* p, float v) { *p = __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 
-__device__ __forceinline__ void ld_vec8(const float* p, float (&f)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-}
-__device__ __forceinline__ void ld_vec8(const uint16_t* p, float (&f)[8]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  f[0] = bf16_lo(a.x); f[1] = bf16_hi(a.x); f[2] = bf16_lo(a.y); f[3] = bf16_hi(a.y);
-  f[4] = bf16_lo(a.z); f[5] = bf16_hi(a.z); f[6] = bf16_lo(a.w); f[7] = bf16_hi(a.w);
-}
-__device__ __forceinline__ void st_vec8(float* p, const float (&f)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(lo)) |
-         ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(hi)) << 16);
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
 }
-__device__ __forceinline__ void st_vec8(uint16_t* p, const float (&f)[8]) {
-  *reinterpret_cast<uint4*>(p) =
-      make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-}
-
 // How a group of `step` threads holds the columns of a row, C a thread: with
 // vector accesses (kVec: D a multiple of 4, rows aligned to 4 elements) in
 // units of 4 columns, unit u of thread i at 4 (i + u step), so that every access
@@ -66,13 +47,14 @@ __device__ __forceinline__ void st_unit(uint16_t* p, float a, float b, float c, 
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(a, b), pack_bf16(c, d));
 }
 
-template <bool kVec, int C, class T>
+// (kAll: all of the thread's columns lie in the row.)
+template <bool kVec, int C, class T, bool kAll = false>
 __device__ __forceinline__ void ld_cols(const T* row, int col0, int step, int D, float (&f)[C]) {
   if constexpr (kVec) {
 #pragma unroll
     for (int u = 0; u < C / 4; ++u) {
       float x[4] = {0.f, 0.f, 0.f, 0.f};
-      if (col0 + 4 * u * step < D) ld_unit(row + col0 + 4 * u * step, x);
+      if (kAll || col0 + 4 * u * step < D) ld_unit(row + col0 + 4 * u * step, x);
 #pragma unroll
       for (int k = 0; k < 4; ++k) f[4 * u + k] = x[k];
     }
@@ -81,12 +63,12 @@ __device__ __forceinline__ void ld_cols(const T* row, int col0, int step, int D,
     for (int k = 0; k < C; ++k) f[k] = col0 + k * step < D ? ld1(row + col0 + k * step) : 0.f;
   }
 }
-template <bool kVec, int C, class T>
+template <bool kVec, int C, class T, bool kAll = false>
 __device__ __forceinline__ void st_cols(T* row, int col0, int step, int D, const float (&f)[C]) {
   if constexpr (kVec) {
 #pragma unroll
     for (int u = 0; u < C / 4; ++u)
-      if (col0 + 4 * u * step < D)
+      if (kAll || col0 + 4 * u * step < D)
         st_unit(row + col0 + 4 * u * step, f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3]);
   } else {
 #pragma unroll

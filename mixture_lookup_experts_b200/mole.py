@@ -589,7 +589,7 @@ def mole_block_norm_forward(x: torch.Tensor, f: torch.Tensor | None = None, w_po
         if x_out is None and (f is not None or res_scale != 1.0):
             x_out = torch.empty_like(x)
         if h is None and w_pre is not None:
-            h = torch.empty((T, D), dtype=h_dtype, device=x.device)
+            h = torch.empty_like(x, dtype=h_dtype)
         _ok(lib.mole_block_norm_forward(_ptr(x), _dt(x), _ptr(f), F32 if f is None else _dt(f), _ptr(w_post),
                                         _ptr(gate), res_scale, _ptr(w_pre), eps, T, D, _ptr(x_out), _ptr(h),
                                         BF16 if h is None else _dt(h), s), "mole_block_norm_forward")
@@ -623,11 +623,11 @@ def mole_block_norm_backward(x_out: torch.Tensor, dx_out: torch.Tensor | None, d
     dev = x_out.device
     with _launching(stream, x_out) as s:
         if dx is None:
-            dx = torch.empty((T, D), dtype=torch.float32, device=dev)
+            dx = torch.empty_like(x_out, dtype=torch.float32)
         if df is None and f is not None:
-            df = torch.empty((T, D), dtype=torch.float32, device=dev)
+            df = torch.empty_like(x_out, dtype=torch.float32)
         if dgate is None and gate is not None:
-            dgate = torch.empty((T,), dtype=torch.float32, device=dev)
+            dgate = torch.empty_like(gate)
         if workspace is None and (dw_post is not None or dw_pre is not None):
             workspace = torch.empty(max(1, lib.mole_block_norm_backward_workspace(T, D)), dtype=torch.uint8,
                                     device=dev)
