@@ -33,11 +33,12 @@ constexpr int kSortCtas = 16;  // 16 measured against 8: 12.1 -> 11.6 us at 1638
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDigits = 256;
+constexpr int kParts = kSortThreads / kDigits;  // groups of warps in a scan over them
 constexpr int kChunkThreads = 128;
 constexpr int kJoinThreads = 128;
-constexpr int kChunkUnits = 2, kChunkSlots = 5, kScalarCols = 8;
+constexpr int kChunkUnits = 2, kChunkSlots = 5, kScalarCols = 4;
 constexpr int64_t kChunkGroups = 1776;  // chunks times slices: 12 CTAs for each of 148 SMs
-constexpr int kSmallTokens = 2048;
+constexpr int kSmallTokens = 1024;
 
 // ---- forward ----
 // blockDim = (tx, 256 / tx): a row slice per group of tx threads, kRows rows in
@@ -97,8 +98,8 @@ __device__ __forceinline__ int2 sort_key(const int32_t* ids, int64_t V, int64_t 
 // Digits and counts of a radix pass run by one CTA (of kSortWarps warps).
 struct SortSmem {
   int hist[kSortWarps][kDigits];  // per warp: its count of a digit, then its offset inside the CTA
-  int psum[kSortThreads / kDigits][kDigits];
-  int tot[kDigits];               // per digit: the CTA's count
+  int psum[kParts][kDigits];
+  int tot[kSortCtas][kDigits];    // per digit: the CTAs' counts (by rank; one CTA: [0])
   int base[kDigits];              // per digit: position of the CTA's first element
   int wsum[kDigits / 32];
 };
@@ -133,9 +134,10 @@ __device__ __forceinline__ void rank_tiles(const int2 (&e)[kHold], int (&rank)[k
   }
 }
 
-// hist (counts per warp) to offsets inside the CTA, and the totals.
-__device__ __forceinline__ void scan_warps(SortSmem& s) {
-  constexpr int kParts = kSortThreads / kDigits, kPartWarps = kSortWarps / kParts;
+// hist (counts per warp) to offsets inside the CTA; returns the CTA's count of
+// the thread's digit (threadIdx.x % kDigits).
+__device__ __forceinline__ int scan_warps(SortSmem& s) {
+  constexpr int kPartWarps = kSortWarps / kParts;
   const int digit = threadIdx.x & (kDigits - 1), part = threadIdx.x / kDigits;
   int c[kPartWarps], run = 0;
 #pragma unroll
@@ -145,13 +147,15 @@ __device__ __forceinline__ void scan_warps(SortSmem& s) {
   }
   s.psum[part][digit] = run;
   __syncthreads();
-  int start = 0;
+  int start = 0, all = 0;
 #pragma unroll
-  for (int p = 0; p < kParts; ++p)
-    if (p < part) start += s.psum[p][digit];
+  for (int p = 0; p < kParts; ++p) {
+    if (p == part) start = all;
+    all += s.psum[p][digit];
+  }
 #pragma unroll
   for (int w = 0; w < kPartWarps; ++w) s.hist[part * kPartWarps + w][digit] = start + c[w];
-  if (part == kParts - 1) s.tot[digit] = start + run;
+  return all;
 }
 
 // base[d] = sum of `all` over the digits before d, plus `before` (threads below
@@ -192,6 +196,7 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
   int2* mine = reinterpret_cast<int2*>(sort_smem + sizeof(SortSmem));  // kLocal: this CTA's elements
   pdl_trigger();  // the chunk kernel may take its place on the other SMs
   cg::cluster_group cluster = cg::this_cluster();
+  auto started = cluster.barrier_arrive();  // waited for before the first access to another CTA's memory
   const int cta = (int)cluster.block_rank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (cta == 0 && threadIdx.x == 0) *a.n_runs = 0;
@@ -229,13 +234,20 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
       rank_tiles<H>(e, rank, hi - i0, shift, s.hist[warp]);
     }
     __syncthreads();
-    scan_warps(s);
-    cluster.sync();  // tot is there (and every element of `mine` is in registers)
+    // the CTA's counts to every CTA of the cluster: written, not read, across
+    // it, so that their way is part of the barrier's
+    const int count = scan_warps(s);
+    if (pass == 0) cluster.barrier_wait(std::move(started));
+#pragma unroll
+    for (int r = 0; r < kSortCtas / kParts; ++r)
+      cluster.map_shared_rank(&s.tot[cta][0], (threadIdx.x / kDigits) * (kSortCtas / kParts) + r)[threadIdx.x &
+                                                                                               (kDigits - 1)] = count;
+    cluster.sync();  // (and every element of `mine` is in registers)
     int before = 0, all = 0;
     if (threadIdx.x < kDigits) {
 #pragma unroll
       for (int r = 0; r < kSortCtas; ++r) {
-        const int x = cluster.map_shared_rank(s.tot, r)[threadIdx.x];
+        const int x = s.tot[r][threadIdx.x];
         if (r < cta) before += x;
         all += x;
       }
@@ -260,8 +272,9 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
         }
       }
     }
-    // the pass's output and the readers of tot are done
-    cluster.sync();
+    // the pass's output is there, and tot has been read (the last pass's output
+    // goes to global memory, and no CTA touches another's memory after it)
+    if (!last) cluster.sync();
   }
 }
 
@@ -279,35 +292,28 @@ struct SumArgs {
   int2* runs;       // and of each {chunk where it begins, id}, in any order
 };
 
-// Rows of dout in order of their runs: batches of kQ tokens have the loads of
-// their rows in flight, and with them those rows of dE whose run ends in the
-// batch (a load inside the sums would stall them once per run).  kAhead: the
-// ids of the next batch are loaded meanwhile.  `at(p)` gives the sorted element p, p < end
-// only; `whole` takes a run that both begins and ends in [p0, p1), `head` the
-// sum of one that entered, `tail` of one that leaves.
-template <bool kVec, class In, int C, int kQ, bool kAhead, class At, class Head, class Tail>
-__device__ __forceinline__ void sum_runs(const In* dout, float* dE, int D, float scale, int V, int64_t p0, int64_t p1,
-                                         int64_t end, int enters, int col0, int step, At at, Head head, Tail tail) {
+// Rows of dout in order of their runs, column by column (any width and
+// alignment): batches of kQ tokens have the loads of their rows in flight, and
+// with them those rows of dE whose run ends in the batch (a load inside the sums
+// would stall them once per run).  `at(p)` gives the sorted element p < end;
+// runs that end in [p0, p1) go to dE, `head` takes the sum of a part that
+// entered, `tail` of one that leaves.
+template <class In, int C, int kQ, class At, class Head, class Tail>
+__device__ __forceinline__ void sum_runs(const In* dout, float* dE, int D, float scale, int V, int p0, int p1, int end, int enters, int col0, int step, At at, Head head, Tail tail) {
   float acc[C];
   int cur = -1;
   int2 e[kQ + 1];
 #pragma unroll
   for (int q = 0; q <= kQ; ++q) e[q] = p0 + q < end ? at(p0 + q) : make_int2(-1, 0);
-  for (int64_t p = p0; p < p1; p += kQ) {
-    RowUnit<kVec, In, C> row[kQ];
-    RowUnit<kVec, float, C> grad[kQ];
+  for (int p = p0; p < p1; p += kQ) {
+    RowUnit<false, In, C> row[kQ];
+    RowUnit<false, float, C> grad[kQ];
 #pragma unroll
     for (int q = 0; q < kQ; ++q)
       if (p + q < p1 && e[q].x != V) {
         row[q].load(dout + (int64_t)e[q].y * D, col0, step, D);
         if (e[q].x != e[q + 1].x && e[q].x != enters) grad[q].load(dE + (int64_t)e[q].x * D, col0, step, D);
       }
-    int2 next[kAhead ? kQ + 1 : 1];
-    if constexpr (kAhead) {
-      next[0] = e[kQ];
-#pragma unroll
-      for (int q = 1; q <= kQ; ++q) next[q] = p + kQ + q < end ? at(p + kQ + q) : make_int2(-1, 0);
-    }
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
       if (p + q >= p1 || e[q].x == V) break;
@@ -324,18 +330,13 @@ __device__ __forceinline__ void sum_runs(const In* dout, float* dE, int D, float
         grad[q].get(g);
 #pragma unroll
         for (int k = 0; k < C; ++k) g[k] = fmaf(scale, acc[k], g[k]);
-        st_cols<kVec>(dE + (int64_t)cur * D, col0, step, D, g);
+        st_cols<false>(dE + (int64_t)cur * D, col0, step, D, g);
       } else if (p + q + 1 == p1) {
         tail(cur, acc);
       }
     }
 #pragma unroll
-    for (int q = 0; q <= kQ; ++q) {
-      if constexpr (kAhead)
-        e[q] = next[q];
-      else
-        e[q] = p + kQ + q < end ? at(p + kQ + q) : make_int2(-1, 0);
-    }
+    for (int q = 0; q <= kQ; ++q) e[q] = p + kQ + q < end ? at(p + kQ + q) : make_int2(-1, 0);
   }
 }
 
@@ -371,6 +372,22 @@ __device__ __forceinline__ Share chunk_share(int n, int chunk, Id id) {
   return s;
 }
 
+// After the sort: the tokens of the chunk and of the next one into es[0] ..
+// es[2 * chunk - 1], and those at -1, 2 * chunk and (es[-2]) -chunk - 1.  Returns
+// the number of tokens in the chunk; all threads of the CTA take part.
+__device__ __forceinline__ int load_share(const SumArgs& a, int64_t c, int2* es) {
+  const int64_t p0 = c * a.chunk;
+  const int n = c < a.n_chunks ? (int)std::min<int64_t>(a.chunk, a.T - p0) : 0;
+  pdl_wait();
+  if (n > 0)
+    for (int i = (int)threadIdx.x - 2; i <= 2 * a.chunk; i += blockDim.x) {
+      const int64_t p = i == -2 ? p0 - a.chunk - 1 : p0 + i;
+      es[i] = p >= 0 && p < a.T ? a.sorted[p] : make_int2(-1, 0);
+    }
+  __syncthreads();
+  return n;
+}
+
 __device__ __forceinline__ void leave_run(const SumArgs& a, int64_t c, int id) {
   if (threadIdx.x == 0 && blockIdx.y == 0) a.runs[atomicAdd(a.n_runs, 1)] = make_int2((int)c, id);
 }
@@ -388,23 +405,13 @@ __global__ void __launch_bounds__(kChunkThreads) embed_chunk_kernel(const SumArg
   extern __shared__ __align__(16) uint8_t chunk_smem[];
   // slot: per unit the threads' columns of dout, then their columns of dE
   const int tid = threadIdx.y * blockDim.x + threadIdx.x;
-  // the tokens of the chunk and of the next one (es[0] .. es[2 * chunk - 1]), and
-  // those at -1, -chunk - 1 and 2 * chunk
   int2* es = reinterpret_cast<int2*>(chunk_smem + (size_t)kSlots * kSlotBytes) +
              (size_t)threadIdx.y * (2 * a.chunk + 3) + 2;
   pdl_trigger();
   const int64_t c = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const int step = blockDim.x;
   const int col0 = blockIdx.y * step * 4 * kUnits + 4 * (int)threadIdx.x;
-  const int64_t p0 = c * a.chunk;
-  const int n = c < a.n_chunks ? (int)std::min<int64_t>(a.chunk, a.T - p0) : 0;
-  pdl_wait();
-  if (n > 0)
-    for (int i = (int)threadIdx.x - 2; i <= 2 * a.chunk; i += step) {
-      const int64_t p = i == -2 ? p0 - a.chunk - 1 : p0 + i;
-      es[i] = p >= 0 && p < a.T ? a.sorted[p] : make_int2(-1, 0);
-    }
-  __syncthreads();
+  const int n = load_share(a, c, es);
   if (n == 0 || col0 >= a.D) return;
   const Share share = chunk_share(n, a.chunk, [&](int i) { return es[i < -1 ? -2 : i].x; });
   const int units = std::min(kUnits, (a.D - col0 + 4 * step - 1) / (4 * step));  // those that begin inside the row
@@ -478,21 +485,20 @@ __global__ void __launch_bounds__(kChunkThreads) embed_chunk_kernel(const SumArg
 // Rows of any width and alignment.
 template <class In>
 __global__ void __launch_bounds__(kChunkThreads) embed_chunk_scalar_kernel(const SumArgs a) {
-  constexpr int C = kScalarCols, kQ = 4;
+  constexpr int C = kScalarCols, kQ = 2;
+  extern __shared__ __align__(16) uint8_t chunk_smem[];
+  int2* es = reinterpret_cast<int2*>(chunk_smem) + (size_t)threadIdx.y * (2 * a.chunk + 3) + 2;
   pdl_trigger();
   const int64_t c = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const int step = blockDim.x;
   const int col0 = blockIdx.y * step * C + (int)threadIdx.x;
-  pdl_wait();
-  if (c >= a.n_chunks || col0 >= a.D) return;
-  const int64_t p0 = c * a.chunk;
-  const Share share = chunk_share((int)std::min<int64_t>(a.chunk, a.T - p0), a.chunk, [&](int i) {
-    return p0 + i >= 0 && p0 + i < a.T ? a.sorted[p0 + i].x : -1;
-  });
+  const int n = load_share(a, c, es);
+  if (n == 0 || col0 >= a.D) return;
+  const Share share = chunk_share(n, a.chunk, [&](int i) { return es[i < -1 ? -2 : i].x; });
   float* part = a.part + 2 * c * a.D;
-  sum_runs<false, In, C, kQ, true>(
-      static_cast<const In*>(a.dout), a.dE, a.D, a.scale, (int)a.V, p0 + share.begin, p0 + share.end, a.T,
-      share.enters, col0, step, [&](int64_t p) { return a.sorted[p]; },
+  sum_runs<In, C, kQ>(
+      static_cast<const In*>(a.dout), a.dE, a.D, a.scale, (int)a.V, share.begin, share.end, 2 * a.chunk + 1,
+      share.enters, col0, step, [&](int i) { return es[i]; },
       [&](const float(&acc)[C]) { st_cols<false>(part, col0, step, a.D, acc); },
       [&](int id, const float(&acc)[C]) {
         st_cols<false>(part + a.D, col0, step, a.D, acc);
@@ -602,9 +608,7 @@ __global__ void __launch_bounds__(kSortThreads, 1)
     __syncwarp();
     rank_tiles<H>(e, rank, T - lo, 8 * pass, s.hist[warp]);
     __syncthreads();
-    scan_warps(s);
-    __syncthreads();
-    scan_digits(s, threadIdx.x < kDigits ? s.tot[threadIdx.x] : 0, 0);
+    scan_digits(s, scan_warps(s), 0);
 #pragma unroll
     for (int j = 0; j < H; ++j)
       if (lo + 32 * j + lane < T) {
@@ -625,9 +629,9 @@ __global__ void __launch_bounds__(kSortThreads, 1)
   float* leaving = entering + 32;
   int owner = -1;  // the id of the run that begins in this share and leaves it
   if (p0 < p1 && col < D)
-    sum_runs<false, In, 1, kQ, false>(
+    sum_runs<In, 1, kQ>(
         dout, dE, D, scale, (int)V, p0, p1, T, p0 > 0 ? sorted[p0 - 1].x : -1, col, 32,
-        [&](int64_t p) { return sorted[p]; }, [&](const float(&acc)[1]) { *entering = acc[0]; },
+        [&](int p) { return sorted[p]; }, [&](const float(&acc)[1]) { *entering = acc[0]; },
         [&](int id, const float(&acc)[1]) {
           owner = id;
           *leaving = acc[0];
@@ -698,14 +702,17 @@ cudaError_t launch_sums(const SumArgs& a, int n_sm, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cudaError_t e;
+  const size_t share_bytes = (size_t)cfg.blockDim.y * (2 * a.chunk + 3) * 8;
   if constexpr (kVec) {
     auto kern = embed_chunk_kernel<In, kChunkUnits, kChunkSlots>;
-    cfg.dynamicSmemBytes = (size_t)kChunkSlots * kChunkUnits * (4 * sizeof(In) + 16) * kChunkThreads +
-                           (size_t)cfg.blockDim.y * (2 * a.chunk + 3) * 8;
+    cfg.dynamicSmemBytes = (size_t)kChunkSlots * kChunkUnits * (4 * sizeof(In) + 16) * kChunkThreads + share_bytes;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kern, a);
   } else {
-    e = cudaLaunchKernelEx(&cfg, embed_chunk_scalar_kernel<In>, a);
+    auto kern = embed_chunk_scalar_kernel<In>;
+    cfg.dynamicSmemBytes = share_bytes;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kern, a);
   }
   if (e != cudaSuccess || a.n_chunks < 3) return e;
   // (a run with parts enters a whole chunk: at most one per two chunks)
