@@ -135,6 +135,13 @@ __device__ __forceinline__ uint32_t encode(const float (&f)[4]) {
   return lo | (hi << 16);
 }
 
+// 1 / x for x that is zero, infinite, NaN or in [2^-126, 2^126] (1 ulp).
+__device__ __forceinline__ float fast_rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // The scale of a block whose largest magnitude has these bits (a NaN stays one).
 __device__ __forceinline__ float block_scale(unsigned bits) {
   const float s = __fmul_rn(__uint_as_float(__reduce_max_sync(0xffffffffu, bits)), kInvE4m3Max);
@@ -189,10 +196,10 @@ __device__ __forceinline__ void step_chunk(const AdamArgs& a, const AdamTensor& 
     }
   }
   const float decay = w.lr * t.weight_decay;
+  float r[kAdamUnits][4];
 #pragma unroll
   for (int u = 0; u < kAdamUnits; ++u) {
     const int64_t e = e0 + 4 * u * kAdamThreads;
-    float r[4];
     unsigned m_max = 0, r_max = 0;
     if constexpr (kState8) {
       decode(mc[u], m[u]);
@@ -208,34 +215,48 @@ __device__ __forceinline__ void step_chunk(const AdamArgs& a, const AdamTensor& 
       g[u][k] *= w.grad;
       m[u][k] = __fadd_rn(__fmul_rn(m[u][k], a.b1), __fmul_rn(g[u][k], a.omb1));
       v[u][k] = __fadd_rn(__fmul_rn(v[u][k], a.b2), __fmul_rn(__fmul_rn(g[u][k], g[u][k]), a.omb2));
-      r[k] = __fsqrt_rn(v[u][k]);
-      const float step = __fdividef(m[u][k], fmaf(r[k], w.root, a.eps));
+      r[u][k] = __fsqrt_rn(v[u][k]);
+      // (the root of a v that is not zero is at least 2^-75: no subnormal here)
+      const float step = m[u][k] * fast_rcp(fmaf(r[u][k], w.root, a.eps));
       p[u][k] = fmaf(-w.step_size, step, fmaf(-decay, p[u][k], p[u][k]));
       if constexpr (kState8) {
         m_max = max(m_max, __float_as_uint(fabsf(m[u][k])));
-        r_max = max(r_max, __float_as_uint(r[k]));
+        r_max = max(r_max, __float_as_uint(r[u][k]));
       }
     }
     if constexpr (kMaster) store_unit<kFull>(t.master + e, cnt[u], p[u]);
     store_unit<kFull>(static_cast<P*>(t.param) + e, cnt[u], p[u]);
     if constexpr (kState8) {
-      const float nm = block_scale(m_max), nv = block_scale(r_max);
-      const float im = __frcp_rn(nm), iv = __frcp_rn(nv);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        m[u][k] = __fmul_rn(m[u][k], im);
-        const float q = __fmul_rn(r[k], iv);
-        v[u][k] = r[k] > 0.f && q < kE4m3Tiny ? kE4m3Tiny : q;
-      }
-      store_codes<kFull>(static_cast<uint8_t*>(t.m) + e, cnt[u], encode(m[u]));
-      store_codes<kFull>(static_cast<uint8_t*>(t.v) + e, cnt[u], encode(v[u]));
-      if (cnt[u] > 0 && (threadIdx.x & 31) == 0) {
-        t.m_scale[e / kAdamBlock] = nm;
-        t.v_scale[e / kAdamBlock] = nv;
-      }
+      sm[u] = block_scale(m_max);
+      sv[u] = block_scale(r_max);
     } else {
       store_unit<kFull>(static_cast<float*>(t.m) + e, cnt[u], m[u]);
       store_unit<kFull>(static_cast<float*>(t.v) + e, cnt[u], v[u]);
+    }
+  }
+  if constexpr (kState8) {
+    // the scales' reciprocals, correctly rounded: one division for the warp's
+    // blocks, a lane each
+    static_assert(kAdamUnits == 2, "four scales");
+    const int lane = threadIdx.x & 31;
+    const float own = lane & 1 ? (lane & 2 ? sv[1] : sv[0]) : (lane & 2 ? sm[1] : sm[0]);
+    const float inv = __frcp_rn(own);
+#pragma unroll
+    for (int u = 0; u < kAdamUnits; ++u) {
+      const int64_t e = e0 + 4 * u * kAdamThreads;
+      const float im = __shfl_sync(0xffffffffu, inv, 2 * u), iv = __shfl_sync(0xffffffffu, inv, 2 * u + 1);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        m[u][k] = __fmul_rn(m[u][k], im);
+        const float q = __fmul_rn(r[u][k], iv);
+        v[u][k] = r[u][k] > 0.f && q < kE4m3Tiny ? kE4m3Tiny : q;
+      }
+      store_codes<kFull>(static_cast<uint8_t*>(t.m) + e, cnt[u], encode(m[u]));
+      store_codes<kFull>(static_cast<uint8_t*>(t.v) + e, cnt[u], encode(v[u]));
+      if (cnt[u] > 0 && lane == 0) {
+        t.m_scale[e / kAdamBlock] = sm[u];
+        t.v_scale[e / kAdamBlock] = sv[u];
+      }
     }
   }
 }
