@@ -287,9 +287,9 @@ struct SumArgs {
   const void* dout;
   float scale;
   float* dE;
-  float* part;  // [n_chunks][2][D]: sums of the run that enters the chunk, of the run that leaves it
-  int* n_runs;      // runs with parts: how many,
-  int2* runs;       // and of each {chunk where it begins, id}, in any order
+  float* part;  // [n_chunks][2][D]: sums of the part that entered the chunk, of the part that leaves it
+  int* n_runs;  // runs with parts: how many,
+  int2* runs;   // and of each {chunk where it begins, id}, in any order
 };
 
 // Rows of dout in order of their runs, column by column (any width and
@@ -299,7 +299,8 @@ struct SumArgs {
 // runs that end in [p0, p1) go to dE, `head` takes the sum of a part that
 // entered, `tail` of one that leaves.
 template <class In, int C, int kQ, class At, class Head, class Tail>
-__device__ __forceinline__ void sum_runs(const In* dout, float* dE, int D, float scale, int V, int p0, int p1, int end, int enters, int col0, int step, At at, Head head, Tail tail) {
+__device__ __forceinline__ void sum_runs(const In* dout, float* dE, int D, float scale, int V, int p0, int p1, int end,
+                                         int enters, int col0, int step, At at, Head head, Tail tail) {
   float acc[C];
   int cur = -1;
   int2 e[kQ + 1];
@@ -398,7 +399,11 @@ __device__ __forceinline__ void leave_run(const SumArgs& a, int64_t c, int id) {
 // registers; with a row come the columns of dE where its run ends.  A thread
 // has kUnits units of 4 columns, 4 * blockDim.x apart: accesses to dout and to
 // dE are both contiguous over a warp, and the bookkeeping of a token serves all
-// of them.
+// of them.  (Loads into registers, 8 tokens at a time: 47 us for 16384 Zipf
+// tokens of 2048 fp32, this form 36; 1, 2 and 4 units and 4 to 14 slots: 2 and 5
+// are the fastest together.)  Bound by HBM for ids that hardly repeat (65536 x
+// 1024 bf16: 70 us against 66 at the copy rate), for text by the last CTAs: 9 us
+// each, which nothing overlaps at the end.
 template <class In, int kUnits, int kSlots>
 __global__ void __launch_bounds__(kChunkThreads) embed_chunk_kernel(const SumArgs a) {
   constexpr int kIn = 4 * sizeof(In), kUnitBytes = kIn + 16, kSlotBytes = kUnits * kUnitBytes * kChunkThreads;
@@ -651,19 +656,22 @@ __global__ void __launch_bounds__(kSortThreads, 1)
 }
 
 // Tokens per chunk: enough (chunk, slice) groups to fill the GPU several times
-// over, few enough partial sums (2 rows of D per chunk) to stay small beside
-// the gradient rows.
+// over (888 to 2368 groups measured within 5 % of each other at 16384 x 2048 and
+// 65536 x 1024), no more than 256, so that the partial sums (2 rows of D per
+// chunk) stay small beside the rows of dout, and no more than leave room for the
+// CTA's groups' tokens in 64 KB of shared memory (narrow rows: up to 128 groups).
 int chunk_tokens(int64_t T, int64_t D) {
   const RowSplit r = row_split(D, 4 * kChunkUnits, kChunkThreads);
   const int64_t groups = std::max<int64_t>(1, kChunkGroups * (kChunkThreads / r.tx) / r.slices);
-  return (int)std::min<int64_t>(256, std::max<int64_t>(8, (T + groups - 1) / groups));
+  const int64_t room = (64 * 1024 / 8 / (kChunkThreads / r.tx) - 3) / 2;
+  return (int)std::min<int64_t>(std::min<int64_t>(256, room), std::max<int64_t>(8, (T + groups - 1) / groups));
 }
 
 struct EmbedWs {
-  int2* buf[2];
+  int2* buf[2];  // [T] sorted elements
   int* n_runs;
-  int2* runs;     // [n_chunks]
-  float* part;
+  int2* runs;    // [n_chunks]
+  float* part;   // [n_chunks][2][D]
 };
 
 size_t carve_embed(void* ws, int64_t T, int64_t D, EmbedWs* w) {
@@ -798,7 +806,7 @@ mole_status embed_backward(const int32_t* ids, int64_t T, const void* dout, bool
     return cuda_status((bf16 ? launch_small<uint16_t> : launch_small<float>)(ids, T, V, passes, dout, (int)D, scale, dE,
                                                                             err, stream));
   const SortArgs sa{ids, T, V, w.buf[0], w.buf[1], passes, w.n_runs, err};
-  if (T <= 1 * kSortCtas * kSortThreads)
+  if (T <= kSortCtas * kSortThreads)
     e = launch_sort<1>(sa, stream);
   else if (T <= 4 * kSortCtas * kSortThreads)
     e = launch_sort<4>(sa, stream);
@@ -806,8 +814,7 @@ mole_status embed_backward(const int32_t* ids, int64_t T, const void* dout, bool
     e = launch_sort<0>(sa, stream);
   if (e != cudaSuccess) return MOLE_ERR_CUDA;
   const int chunk = chunk_tokens(T, D);
-  const SumArgs a{w.buf[0], T, V, (int)D, chunk, (T + chunk - 1) / chunk, dout, scale, dE, w.part, w.n_runs,
-            w.runs};
+  const SumArgs a{w.buf[0], T, V, (int)D, chunk, (T + chunk - 1) / chunk, dout, scale, dE, w.part, w.n_runs, w.runs};
   if (bf16)
     e = vec ? launch_sums<true, uint16_t>(a, n_sm, stream) : launch_sums<false, uint16_t>(a, n_sm, stream);
   else

@@ -1,6 +1,6 @@
-// rows.cuh -- access to rows of D elements by groups of threads, 8 columns a
-// thread, fp32 or bf16: shared by the embedding (embed.cu) and the block norms
-// (norm.cu).
+// rows.cuh -- access to rows of D elements, fp32 or bf16, by groups of threads,
+// in units of 4 elements: shared by the embedding (embed.cu), the block norms
+// (norm.cu) and the optimizer (adamw.cu).
 #pragma once
 
 #include "common.cuh"
@@ -25,6 +25,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&p);
 }
+
 // How a group of `step` threads holds the columns of a row, C a thread: with
 // vector accesses (kVec: D a multiple of 4, rows aligned to 4 elements) in
 // units of 4 columns, unit u of thread i at 4 (i + u step), so that every access

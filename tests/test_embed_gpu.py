@@ -177,6 +177,20 @@ def test_backward_large_batch_and_vocabulary(mole):
     assert bool(((dE.double() - want).abs() <= 5004 * ref.U * mag).all())
 
 
+@pytest.mark.parametrize("T,V,D", [(8_000_000, 3, 4), (3_000_000, 1000, 8), (300_000, 70, 1030)])
+def test_backward_very_large_batches(mole, T, V, D):
+    # narrow rows (many chunks per CTA) and chunks of many tokens, checked by torch in fp64
+    ids = torch.randint(0, V, (T,), dtype=torch.int32, device="cuda")
+    dout = torch.randn(T, D, device="cuda").to(BF16)
+    dE = torch.zeros(V, D, device="cuda")
+    mole.mole_embed_backward(ids, dout, dE)
+    assert mole.mole_check() == 0
+    want = torch.zeros(V, D, dtype=torch.float64, device="cuda").index_add_(0, ids, dout.double())
+    mag = torch.zeros(V, D, dtype=torch.float64, device="cuda").index_add_(0, ids, dout.double().abs())
+    count = torch.bincount(ids.long(), minlength=V)[:, None]
+    assert bool(((dE.double() - want).abs() <= (count + 4) * ref.U * mag).all())
+
+
 def test_backward_on_a_stream_and_in_a_graph(mole):
     rng = np.random.default_rng(8)
     T, V, D = 3000, 500, 128
