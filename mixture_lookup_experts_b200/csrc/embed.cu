@@ -346,15 +346,15 @@ __device__ __forceinline__ void sum_runs(const In* dout, float* dE, int D, float
 // change at each border so that only runs longer than a chunk have parts: a run
 // that crosses one border belongs whole to the chunk where it begins.
 struct Share {
-  int begin, end;      // tokens of the share, from the chunk's first one; end may pass the chunk
-  int enters, leaves;  // ids (or -1): of a part that entered the chunk, of one that leaves it
+  int begin, end;  // tokens of the share, from the chunk's first one; end may pass the chunk
+  int enters;      // the id (or -1) of a part that entered the chunk
 };
 
 // `id(i)`: id of the i-th token from the chunk's first, -1 outside the batch,
 // for i from -chunk - 1 to 2 * chunk; n tokens in the chunk.
 template <class Id>
 __device__ __forceinline__ Share chunk_share(int n, int chunk, Id id) {
-  Share s{0, n, -1, -1};
+  Share s{0, n, -1};
   const int first = id(0), last = id(n - 1);
   if (id(-1) == first) {
     // one border crossed: it begins in the chunk before this one and ends here
@@ -364,12 +364,9 @@ __device__ __forceinline__ Share chunk_share(int n, int chunk, Id id) {
       s.enters = first;
     }
   }
-  if (n == chunk && id(n) == last && s.enters != last) {
-    if (id(2 * chunk) == last)
-      s.leaves = last;
-    else
-      while (id(s.end) == last) ++s.end;
-  }
+  // (a run that reaches behind the next chunk leaves a part)
+  if (n == chunk && id(n) == last && s.enters != last && id(2 * chunk) != last)
+    while (id(s.end) == last) ++s.end;
   return s;
 }
 
@@ -714,16 +711,18 @@ cudaError_t launch_sums(const SumArgs& a, int n_sm, cudaStream_t stream) {
   if constexpr (kVec) {
     auto kern = embed_chunk_kernel<In, kChunkUnits, kChunkSlots>;
     cfg.dynamicSmemBytes = (size_t)kChunkSlots * kChunkUnits * (4 * sizeof(In) + 16) * kChunkThreads + share_bytes;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+    e = allow_smem(kern);
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kern, a);
   } else {
     auto kern = embed_chunk_scalar_kernel<In>;
     cfg.dynamicSmemBytes = share_bytes;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+    e = allow_smem(kern);
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kern, a);
   }
-  if (e != cudaSuccess || a.n_chunks < 3) return e;
-  // (a run with parts enters a whole chunk: at most one per two chunks)
+  if (e != cudaSuccess) return e;
+  // Always launched (more than kSmallTokens make at least 4 chunks): the chunk
+  // kernel lets the kernel behind it start early, which must be one that waits.
+  // A run with parts enters a whole chunk: at most one per two chunks.
   const int64_t items = (a.n_chunks / 2) * ((a.D + 127) / 128);
   return launch_pdl(embed_join_kernel<kVec>, (unsigned)std::min<int64_t>(items, (int64_t)n_sm * 8), kJoinThreads, 0,
                     stream, a);
@@ -732,8 +731,7 @@ cudaError_t launch_sums(const SumArgs& a, int n_sm, cudaStream_t stream) {
 template <int kHold>
 cudaError_t launch_sort(const SortArgs& a, cudaStream_t stream) {
   const int smem = (int)sizeof(SortSmem) + kHold * kSortThreads * (int)sizeof(int2);
-  const cudaError_t e =
-      cudaFuncSetAttribute(embed_sort_kernel<kHold>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_smem(embed_sort_kernel<kHold>);
   if (e != cudaSuccess) return e;
   cudaFuncSetAttribute(embed_sort_kernel<kHold>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   embed_sort_kernel<kHold><<<kSortCtas, kSortThreads, smem, stream>>>(a);
@@ -744,7 +742,7 @@ template <class In>
 cudaError_t launch_small(const int32_t* ids, int64_t T, int64_t V, int passes, const void* dout, int D, float scale,
                          float* dE, unsigned* err, cudaStream_t stream) {
   const int smem = (int)sizeof(SortSmem) + kSmallTokens * 8 + kSortWarps * 64 * 4;
-  const cudaError_t e = cudaFuncSetAttribute(embed_small_kernel<In>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_smem(embed_small_kernel<In>);
   if (e != cudaSuccess) return e;
   embed_small_kernel<In><<<(unsigned)((D + 31) / 32), kSortThreads, smem, stream>>>(
       ids, (int)T, V, passes, static_cast<const In*>(dout), D, scale, dE, err);

@@ -150,6 +150,13 @@ RowSplit row_split(int64_t D, int unit, int max_tx) {
   return {tx, (int)((units + tx - 1) / tx)};
 }
 
+// Lets `kern` have up to 220 KB of dynamic shared memory: always the same
+// number, so that calls from several host threads do not lower each other's.
+template <class K>
+cudaError_t allow_smem(K kern) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+}
+
 // Whether vector accesses (units of 4 columns) can start at p.
 bool aligned_rows(const void* p, bool bf16) { return bf16 ? aligned8(p) : aligned16(p); }
 

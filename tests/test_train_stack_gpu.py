@@ -101,3 +101,82 @@ def test_training_step(mole, oracle_mod, T, V, D, N, Dr):
     # ids that the batch does not hold keep their rows
     rest = dev(np.setdiff1d(np.arange(V), ids))
     assert torch.equal(masters["E"][rest].double().cpu(), torch.from_numpy(before["E"])[rest.cpu()])
+
+
+def test_calls_from_two_threads_on_two_streams(mole):
+    """The same calls at the same time, of different sizes, each thread with
+    its stream: the results are those of the calls one by one."""
+    import threading
+    sizes = [(3000, 512), (1500, 2048)]
+    V = 700
+
+    def make(T, D):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(T)
+        rnd = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+        ids = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+        return dict(ids=ids, x=rnd(T, D), f=rnd(T, D), c=rnd(T, D), w=rnd(D), E=rnd(V, D))
+
+    def run(d, stream):
+        T, D = d["x"].shape
+        with torch.cuda.stream(stream):
+            dE, dw, p, m, v = (torch.zeros(s, device="cuda") for s in ((V, D), (D,), (V, D), (V, D), (V, D)))
+            out = mole.mole_embed_forward(d["ids"], d["E"], 2.0)
+            x1, h = mole.mole_block_norm_forward(d["x"], d["f"], d["w"], None, 0.5, d["w"])
+            dx, df, _ = mole.mole_block_norm_backward(x1, d["c"], d["c"], d["f"], d["w"], None, 0.5, d["w"], dw_pre=dw,
+                                                      dw_post=dw.clone())
+            mole.mole_embed_backward(d["ids"], dx, dE)
+            mole.mole_adamw_step([p], [dE], [m], [v])
+        return out, x1, h, dx, df, dw, dE, p
+
+    data = [make(*s) for s in sizes]
+    torch.cuda.synchronize()
+    want = [run(d, torch.cuda.current_stream()) for d in data]
+    torch.cuda.synchronize()
+    got, errors = [None, None], []
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            for _ in range(30):
+                got[i] = run(data[i], stream)
+            stream.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    assert mole.mole_check() == 0
+    for a, b in zip(want, got):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+
+
+def test_norm_backward_before_kernels_that_start_early(mole):
+    """Without weight gradients the backward is one kernel; the library's other
+    kernels behind it (a row prefetch, a combine: both may start early) still
+    find its results."""
+    T, V, D, N = 20000, 300, 512, 8
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    x, f, c, w = rnd(T, D), rnd(T, D), rnd(T, D), rnd(D)
+    lut, Wr = rnd(V, N, D).to(torch.bfloat16), rnd(D, N)
+    lut32 = lut.float()
+    ids = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    _, df, _ = mole.mole_block_norm_backward(x, c, c, f, w, None, 1.0, w)
+    torch.cuda.synchronize()
+    want = mole.mole_lookup_combine(ids, df, Wr, lut32)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        out = torch.zeros_like(df)
+        mole.mole_block_norm_backward(x, c, c, f, w, None, 1.0, w, df=out)
+        mole.mole_prefetch_rows(ids, [lut])
+        got = mole.mole_lookup_combine(ids, out, Wr, lut32)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    assert mole.mole_check() == 0
