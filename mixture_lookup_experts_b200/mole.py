@@ -482,38 +482,41 @@ def mole_prefetch_rows(ids: torch.Tensor, tables, stream=None) -> None:
 # These calls check shapes, types and devices, and run on the device that holds
 # their tensors: `stream` (default: that device's current stream) gets the
 # kernels, and what the call allocates for itself is allocated for that stream.
+# Their checks are written for few Python operations: a small call is bound by
+# its host time.
 
 @contextlib.contextmanager
 def _on_stream(stream, dev: torch.device):
-    """The tensors' device and `stream` made current; gives the stream handle."""
+    """The device and `stream` (if any) made current."""
     with torch.cuda.device(dev):
         if stream is None:
-            yield torch.cuda.current_stream(dev).cuda_stream
+            yield
             return
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream), device=dev)
         if stream.device != dev:
             raise ValueError(f"stream of {stream.device}, tensors on {dev}")
         with torch.cuda.stream(stream):
-            yield stream.cuda_stream
+            yield
 
 
-def _launching(stream, like: torch.Tensor):
-    """A context in which the kernels of `like`'s device and `stream` are
-    launched.  In the usual case (the current stream of the current device)
-    nothing has to change: the handle alone (5 us less per call)."""
-    dev = like.device
-    if stream is None and torch._C._cuda_getDevice() == dev.index:
-        return contextlib.nullcontext(torch._C._cuda_getCurrentRawStream(dev.index))
-    return _on_stream(stream, dev)
+def _elsewhere(stream, dev: int) -> bool:
+    """Whether a call has to make another stream or device current first."""
+    return stream is not None or torch._C._cuda_getDevice() != dev
 
 
-def _expect(name: str, t, like: torch.Tensor, shape=None, dtypes=None) -> None:
+def _device_of(name: str, t: torch.Tensor) -> int:
+    at = t.get_device()
+    if at < 0:
+        raise ValueError(f"{name} is on {t.device}, expected a CUDA device, the same for all tensors")
+    return at
+
+
+def _expect(name: str, t, dev: int, shape=None, dtypes=None) -> None:
     """A tensor argument's device, layout, shape and type (None passes)."""
     if t is None:
         return
-    at = t.get_device()  # -1: not a CUDA tensor
-    if at < 0 or at != like.get_device():
+    if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, expected a CUDA device, the same for all tensors")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -532,16 +535,22 @@ _DT = {torch.float32: F32, torch.bfloat16: BF16}
 def mole_embed_forward(ids: torch.Tensor, E: torch.Tensor, scale: float = 1.0, out: torch.Tensor | None = None,
                        out_dtype=None, stream=None) -> torch.Tensor:
     """out[t] = scale * E[ids[t]] (fp32 or bf16; out in E's type unless asked otherwise)."""
+    dev = _device_of("E", E)
+    if _elsewhere(stream, dev):
+        with _on_stream(stream, E.device):
+            return mole_embed_forward(ids, E, scale, out, out_dtype)
     T = ids.numel()
     V, D = E.shape
-    _expect("E", E, E, None, _ROWS)
-    _expect("ids", ids, E, None, _INT32)
-    _expect("out", out, E, (T, D), _ROWS if out_dtype is None else (out_dtype,))
-    with _launching(stream, E) as s:
-        if out is None:
-            out = torch.empty((T, D), dtype=out_dtype or E.dtype, device=E.device)
-        _ok(lib.mole_embed_forward(_ptr(ids), T, _ptr(E), V, D, scale, _dt(E), _ptr(out), _dt(out), s),
-            "mole_embed_forward")
+    _expect("E", E, dev, None, _ROWS)
+    _expect("ids", ids, dev, None, _INT32)
+    if out is None:
+        out = torch.empty((T, D), dtype=out_dtype or E.dtype, device=E.device)
+        if out.dtype not in _DT:
+            raise TypeError(f"out_dtype is {out_dtype}")
+    else:
+        _expect("out", out, dev, (T, D), _ROWS if out_dtype is None else (out_dtype,))
+    _ok(lib.mole_embed_forward(ids.data_ptr(), T, E.data_ptr(), V, D, scale, _DT[E.dtype], out.data_ptr(),
+                               _DT[out.dtype], torch._C._cuda_getCurrentRawStream(dev)), "mole_embed_forward")
     return out
 
 
@@ -552,18 +561,24 @@ def mole_embed_backward_workspace(T: int, D: int) -> int:
 def mole_embed_backward(ids: torch.Tensor, dout: torch.Tensor, dE: torch.Tensor, scale: float = 1.0,
                         workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """dE[ids[t]] += scale * dout[t] (dE fp32; the same bits on every run); returns dE."""
+    dev = _device_of("dE", dE)
+    if _elsewhere(stream, dev):
+        with _on_stream(stream, dE.device):
+            return mole_embed_backward(ids, dout, dE, scale, workspace)
     T = ids.numel()
     V, D = dE.shape
-    _expect("dE", dE, dE, None, _FP32)
-    _expect("ids", ids, dE, None, _INT32)
-    _expect("dout", dout, dE, (T, D), _ROWS)
-    _expect("workspace", workspace, dE)
-    with _launching(stream, dE) as s:
-        if workspace is None:
-            workspace = torch.empty(max(1, lib.mole_embed_backward_workspace(T, D)), dtype=torch.uint8,
-                                    device=dE.device)
-        _ok(lib.mole_embed_backward(_ptr(ids), T, _ptr(dout), _dt(dout), V, D, scale, _ptr(dE), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), s), "mole_embed_backward")
+    _expect("dE", dE, dev, None, _FP32)
+    _expect("ids", ids, dev, None, _INT32)
+    _expect("dout", dout, dev, (T, D), _ROWS)
+    if workspace is None:
+        nbytes = lib.mole_embed_backward_workspace(T, D)
+        workspace = torch.empty(max(1, nbytes), dtype=torch.uint8, device=dE.device)
+    else:
+        _expect("workspace", workspace, dev)
+        nbytes = workspace.numel() * workspace.element_size()
+    _ok(lib.mole_embed_backward(ids.data_ptr(), T, dout.data_ptr(), _DT[dout.dtype], V, D, scale, dE.data_ptr(),
+                                workspace.data_ptr(), nbytes, torch._C._cuda_getCurrentRawStream(dev)),
+        "mole_embed_backward")
     return dE
 
 
@@ -577,22 +592,28 @@ def mole_block_norm_forward(x: torch.Tensor, f: torch.Tensor | None = None, w_po
     x_out may be x), else it is x itself; h is made where w_pre is given, else
     None.
     """
-    T, D = x.shape
-    _expect("x", x, x, None, _ROWS)
-    _expect("f", f, x, (T, D), _ROWS)
-    _expect("w_post", w_post, x, (D,), _FP32)
-    _expect("gate", gate, x, (T,), _FP32)
-    _expect("w_pre", w_pre, x, (D,), _FP32)
-    _expect("x_out", x_out, x, (T, D), (x.dtype,))
-    _expect("h", h, x, (T, D), _ROWS)
-    with _launching(stream, x) as s:
-        if x_out is None and (f is not None or res_scale != 1.0):
-            x_out = torch.empty_like(x)
-        if h is None and w_pre is not None:
-            h = torch.empty_like(x, dtype=h_dtype)
-        _ok(lib.mole_block_norm_forward(_ptr(x), _dt(x), _ptr(f), F32 if f is None else _dt(f), _ptr(w_post),
-                                        _ptr(gate), res_scale, _ptr(w_pre), eps, T, D, _ptr(x_out), _ptr(h),
-                                        BF16 if h is None else _dt(h), s), "mole_block_norm_forward")
+    dev = _device_of("x", x)
+    if _elsewhere(stream, dev):
+        with _on_stream(stream, x.device):
+            return mole_block_norm_forward(x, f, w_post, gate, res_scale, w_pre, eps, x_out, h, h_dtype)
+    T, D = shape = x.shape
+    _expect("x", x, dev, None, _ROWS)
+    _expect("f", f, dev, shape, _ROWS)
+    _expect("w_post", w_post, dev, (D,), _FP32)
+    _expect("gate", gate, dev, (T,), _FP32)
+    _expect("w_pre", w_pre, dev, (D,), _FP32)
+    _expect("x_out", x_out, dev, shape, (x.dtype,))
+    _expect("h", h, dev, shape, _ROWS)
+    if x_out is None and (f is not None or res_scale != 1.0):
+        x_out = torch.empty_like(x)
+    if h is None and w_pre is not None:
+        if h_dtype not in _DT:
+            raise TypeError(f"h_dtype is {h_dtype}")
+        h = torch.empty_like(x, dtype=h_dtype)
+    _ok(lib.mole_block_norm_forward(x.data_ptr(), _DT[x.dtype], _ptr(f), F32 if f is None else _DT[f.dtype],
+                                    _ptr(w_post), _ptr(gate), res_scale, _ptr(w_pre), eps, T, D, _ptr(x_out),
+                                    _ptr(h), BF16 if h is None else _DT[h.dtype],
+                                    torch._C._cuda_getCurrentRawStream(dev)), "mole_block_norm_forward")
     return (x if x_out is None else x_out), h
 
 
@@ -610,33 +631,43 @@ def mole_block_norm_backward(x_out: torch.Tensor, dx_out: torch.Tensor | None, d
     """(dx, df, dgate) of mole_block_norm_forward from the gradients of its two
     outputs; dw_post and dw_pre are added to where given.  df is made where f
     is given, dgate where gate is."""
-    T, D = x_out.shape
-    _expect("x_out", x_out, x_out, None, _ROWS)
-    _expect("f", f, x_out, (T, D), _ROWS)
-    for name, t in (("dx_out", dx_out), ("dh", dh), ("dx", dx), ("df", df)):
-        _expect(name, t, x_out, (T, D), _FP32)
-    for name, t in (("w_post", w_post), ("w_pre", w_pre), ("dw_post", dw_post), ("dw_pre", dw_pre)):
-        _expect(name, t, x_out, (D,), _FP32)
-    for name, t in (("gate", gate), ("dgate", dgate)):
-        _expect(name, t, x_out, (T,), _FP32)
-    _expect("workspace", workspace, x_out)
-    dev = x_out.device
-    with _launching(stream, x_out) as s:
-        if dx is None:
-            dx = torch.empty_like(x_out, dtype=torch.float32)
-        if df is None and f is not None:
-            df = torch.empty_like(x_out, dtype=torch.float32)
-        if dgate is None and gate is not None:
-            dgate = torch.empty_like(gate)
-        if workspace is None and (dw_post is not None or dw_pre is not None):
-            workspace = torch.empty(max(1, lib.mole_block_norm_backward_workspace(T, D)), dtype=torch.uint8,
-                                    device=dev)
-        _ok(lib.mole_block_norm_backward(_ptr(x_out), _dt(x_out), _ptr(f), F32 if f is None else _dt(f),
-                                         _ptr(w_post), _ptr(gate), res_scale, _ptr(w_pre), eps, T, D, _ptr(dx_out),
-                                         _ptr(dh), _ptr(dx), _ptr(df), _ptr(dgate), _ptr(dw_post), _ptr(dw_pre),
-                                         _ptr(workspace),
-                                         0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                         s), "mole_block_norm_backward")
+    dev = _device_of("x_out", x_out)
+    if _elsewhere(stream, dev):
+        with _on_stream(stream, x_out.device):
+            return mole_block_norm_backward(x_out, dx_out, dh, f, w_post, gate, res_scale, w_pre, eps, dx, df, dgate,
+                                            dw_post, dw_pre, workspace)
+    T, D = shape = x_out.shape
+    per_column = (D,)
+    _expect("x_out", x_out, dev, None, _ROWS)
+    _expect("f", f, dev, shape, _ROWS)
+    _expect("dx_out", dx_out, dev, shape, _FP32)
+    _expect("dh", dh, dev, shape, _FP32)
+    _expect("w_post", w_post, dev, per_column, _FP32)
+    _expect("w_pre", w_pre, dev, per_column, _FP32)
+    _expect("dw_post", dw_post, dev, per_column, _FP32)
+    _expect("dw_pre", dw_pre, dev, per_column, _FP32)
+    _expect("gate", gate, dev, (T,), _FP32)
+    _expect("dgate", dgate, dev, (T,), _FP32)
+    _expect("dx", dx, dev, shape, _FP32)
+    _expect("df", df, dev, shape, _FP32)
+    _expect("workspace", workspace, dev)
+    if dx is None:
+        dx = torch.empty_like(x_out, dtype=torch.float32)
+    if df is None and f is not None:
+        df = torch.empty_like(x_out, dtype=torch.float32)
+    if dgate is None and gate is not None:
+        dgate = torch.empty_like(gate)
+    nbytes = 0
+    if workspace is not None:
+        nbytes = workspace.numel() * workspace.element_size()
+    elif dw_post is not None or dw_pre is not None:
+        nbytes = lib.mole_block_norm_backward_workspace(T, D)
+        workspace = torch.empty(max(1, nbytes), dtype=torch.uint8, device=x_out.device)
+    _ok(lib.mole_block_norm_backward(x_out.data_ptr(), _DT[x_out.dtype], _ptr(f), F32 if f is None else _DT[f.dtype],
+                                     _ptr(w_post), _ptr(gate), res_scale, _ptr(w_pre), eps, T, D, _ptr(dx_out),
+                                     _ptr(dh), dx.data_ptr(), _ptr(df), _ptr(dgate), _ptr(dw_post), _ptr(dw_pre),
+                                     _ptr(workspace), nbytes, torch._C._cuda_getCurrentRawStream(dev)),
+        "mole_block_norm_backward")
     return dx, df, dgate
 
 
@@ -659,20 +690,19 @@ _DTYPE = operator.attrgetter("dtype")
 assert _ADAMW_TENSOR.size == ctypes.sizeof(AdamWTensor)
 
 
-def _addresses(name: str, tensors, sizes, like: torch.Tensor, dtypes, optional=False):
+def _addresses(name: str, tensors, sizes, dev: int, dtypes, optional=False):
     """The tensors' addresses (0 for None, where allowed), all of them checked
     at once: a list of small tensors costs its user host time."""
-    dev = like.get_device()
     if optional:
         given = [(t, k) for t, k in zip(tensors, sizes) if t is not None]
         tensors_given, sizes = [t for t, _ in given], [k for _, k in given]
     else:
         tensors_given = tensors
     of = torch.Tensor
-    if (list(map(of.numel, tensors_given)) != sizes or dev < 0 or not {dev}.issuperset(map(of.get_device, tensors_given))
+    if (list(map(of.numel, tensors_given)) != sizes or not {dev}.issuperset(map(of.get_device, tensors_given))
             or not set(dtypes).issuperset(map(_DTYPE, tensors_given)) or not all(map(of.is_contiguous, tensors_given))):
         for i, (t, k) in enumerate(zip(tensors_given, sizes)):  # which one, and why
-            _expect(f"{name}[{i}]", t, like, None, dtypes)
+            _expect(f"{name}[{i}]", t, dev, None, dtypes)
             if t.numel() != k:
                 raise ValueError(f"{name}[{i}] has {t.numel()} elements, expected {k}")
     if optional:
@@ -701,33 +731,39 @@ def mole_adamw_step(params, grads, ms, vs, masters=None, m_scales=None, v_scales
         raise ValueError("lists of different lengths")
     if n == 0:
         return
-    first = params[0]
     state8 = ms[0].dtype == torch.float8_e4m3fn
     states = (torch.float8_e4m3fn,) if state8 else _FP32
     if state8 != (m_scales is not none) or state8 != (v_scales is not none):
         raise ValueError("m_scales and v_scales belong to 8-bit states, and 8-bit states need them")
+    dev = _device_of("params[0]", params[0])
+    if _elsewhere(stream, dev):
+        with _on_stream(stream, params[0].device):
+            return mole_adamw_step(params, grads, ms, vs, masters if masters is not none else None,
+                                   m_scales if m_scales is not none else None,
+                                   v_scales if v_scales is not none else None, decay, lr, beta1, beta2, eps, step,
+                                   lr_dev, grad_scale)
     sizes = list(map(torch.Tensor.numel, params))
     blocks = [(k + ADAMW_BLOCK - 1) // ADAMW_BLOCK for k in sizes] if state8 else None
-    table = zip(_addresses("params", params, sizes, first, _ROWS), _addresses("grads", grads, sizes, first, _ROWS),
-                masters if masters is none else _addresses("masters", masters, sizes, first, _FP32, optional=True),
-                _addresses("ms", ms, sizes, first, states), _addresses("vs", vs, sizes, first, states),
-                _addresses("m_scales", m_scales, blocks, first, _FP32) if state8 else none,
-                _addresses("v_scales", v_scales, blocks, first, _FP32) if state8 else none,
+    table = zip(_addresses("params", params, sizes, dev, _ROWS), _addresses("grads", grads, sizes, dev, _ROWS),
+                masters if masters is none else _addresses("masters", masters, sizes, dev, _FP32, optional=True),
+                _addresses("ms", ms, sizes, dev, states), _addresses("vs", vs, sizes, dev, states),
+                _addresses("m_scales", m_scales, blocks, dev, _FP32) if state8 else none,
+                _addresses("v_scales", v_scales, blocks, dev, _FP32) if state8 else none,
                 sizes, decay, map(_DT.__getitem__, map(_DTYPE, params)),
                 map(_DT.__getitem__, map(_DTYPE, grads)))
     arr = b"".join(itertools.starmap(_ADAMW_TENSOR.pack, table))
     cfg = AdamWConfig(lr=lr, beta1=beta1, beta2=beta2, eps=eps, state8=int(state8))
     if isinstance(step, torch.Tensor):
-        _expect("step", step.view(-1), first, (1,), (torch.int64,))
+        _expect("step", step.view(-1), dev, (1,), (torch.int64,))
         cfg.step_dev = step.data_ptr()
     else:
         cfg.step = step
     for name, t, field in (("lr_dev", lr_dev, "lr_dev"), ("grad_scale", grad_scale, "grad_scale_dev")):
         if t is not None:
-            _expect(name, t.view(-1), first, (1,), _FP32)
+            _expect(name, t.view(-1), dev, (1,), _FP32)
             setattr(cfg, field, t.data_ptr())
-    with _launching(stream, first) as s:
-        _ok(lib.mole_adamw_step(arr, n, ctypes.addressof(cfg), s), "mole_adamw_step")
+    _ok(lib.mole_adamw_step(arr, n, ctypes.addressof(cfg), torch._C._cuda_getCurrentRawStream(dev)),
+        "mole_adamw_step")
 
 
 def mole_check(stream=None, timeout_ms: int = 10000) -> int:
