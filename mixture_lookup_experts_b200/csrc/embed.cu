@@ -35,7 +35,7 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDigits = 256;
 constexpr int kParts = kSortThreads / kDigits;  // groups of warps in a scan over them
 constexpr int kChunkThreads = 128;
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 256;
 constexpr int kChunkUnits = 2, kChunkSlots = 5, kScalarCols = 4;
 constexpr int64_t kChunkGroups = 1776;  // chunks times slices: 12 CTAs for each of 148 SMs
 constexpr int kSmallTokens = 1024;
@@ -525,9 +525,10 @@ __device__ __forceinline__ int64_t chunks_entered(const SumArgs& a, int64_t c, i
 // Step 3: the parts of the long runs, in chunk order, onto dE.  (The order of
 // the list of runs does not matter: each has its own row.)  Item = (run, 128
 // columns), a CTA each: its warps take the parts in contiguous shares, whose
-// sums are added in order.
+// sums are added in order.  Bound by the chain of loads; 8 warps a CTA: 9600
+// tokens of 544 ids 23.2 us, 4 warps 25.6, 16 warps 22.6 (but text 55 against 53).
 template <bool kVec>
-__global__ void __launch_bounds__(kJoinThreads, 8) embed_join_kernel(const SumArgs a) {
+__global__ void __launch_bounds__(kJoinThreads, 4) embed_join_kernel(const SumArgs a) {
   constexpr int C = 4, kWarpsJ = kJoinThreads / 32, kQ = 8;
   __shared__ float sums[kWarpsJ][C][32];
   pdl_wait();
@@ -724,7 +725,7 @@ cudaError_t launch_sums(const SumArgs& a, int n_sm, cudaStream_t stream) {
   // kernel lets the kernel behind it start early, which must be one that waits.
   // A run with parts enters a whole chunk: at most one per two chunks.
   const int64_t items = (a.n_chunks / 2) * ((a.D + 127) / 128);
-  return launch_pdl(embed_join_kernel<kVec>, (unsigned)std::min<int64_t>(items, (int64_t)n_sm * 8), kJoinThreads, 0,
+  return launch_pdl(embed_join_kernel<kVec>, (unsigned)std::min<int64_t>(items, (int64_t)n_sm * 4), kJoinThreads, 0,
                     stream, a);
 }
 

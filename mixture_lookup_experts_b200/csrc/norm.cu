@@ -76,28 +76,22 @@ __device__ __forceinline__ void row_sums(float (&v)[K], float4* red) {
 
 // A thread's columns of a row on their way through shared memory (cp.async;
 // each thread reads back its own copies only).  at: the thread's place in the
-// stage's area of this tensor, which lies there as in the row.  kFull: the
-// threads' columns are exactly the row's.
-template <bool kFull, int C, class T>
+// stage's area of this tensor, which lies there as in the row.
+template <int kSure, int C, class T>
 __device__ __forceinline__ void stage_put(uint8_t* at, const T* row, int col0, int step, int D) {
 #pragma unroll
   for (int u = 0; u < C / 4; ++u)
-    if (kFull || col0 + 4 * u * step < D) cp_async<4 * sizeof(T)>(at + u * step * 4 * sizeof(T), row + 4 * u * step);
+    if (u < kSure || col0 + 4 * u * step < D) cp_async<4 * sizeof(T)>(at + u * step * 4 * sizeof(T), row + 4 * u * step);
 }
-template <bool kFull, int C, class T>
+template <int kSure, int C, class T>
 __device__ __forceinline__ void stage_get(const uint8_t* at, int col0, int step, int D, float (&f)[C]) {
 #pragma unroll
   for (int u = 0; u < C / 4; ++u) {
     float x[4] = {0.f, 0.f, 0.f, 0.f};
-    if (kFull || col0 + 4 * u * step < D) ld_unit(reinterpret_cast<const T*>(at + u * step * 4 * sizeof(T)), x);
+    if (u < kSure || col0 + 4 * u * step < D) ld_unit(reinterpret_cast<const T*>(at + u * step * 4 * sizeof(T)), x);
 #pragma unroll
     for (int k = 0; k < 4; ++k) f[4 * u + k] = x[k];
   }
-}
-
-template <bool kVec, bool kFull, int C>
-__device__ __forceinline__ void ld_weights(const float* w, int col0, int step, int D, float (&f)[C]) {
-  ld_cols<kVec, C, float, kVec && kFull>(w, col0, step, D, f);
 }
 
 struct NormFwd {
@@ -115,11 +109,14 @@ struct NormFwd {
 
 // A CTA has a row at a time, C columns a thread.  kStages > 0: rows come through
 // shared memory, kStages - 1 of them ahead of the one in work (loads of a row
-// then overlap the sums and stores of the one before; with 2, 3 and 4 stages
-// 78.7, 80.0 and 88.5 us at 8 columns a thread); kStages == 0: straight into
-// registers.
+// then overlap the sums and stores of the one before); kStages == 0: straight
+// into registers.  Stages and registers together: rows of 16 columns a thread
+// have 3 stages (16384 x 2048 fp32 75 to 76 us whatever the tensors' addresses;
+// with 2, 74 to 86), fewer columns 2 (16384 x 768 32.5 us, with 3 34.2); 85
+// registers a thread leave room for 6 CTAs of 4 warps.
 template <bool kVec, int C, int kStages, int kThreads, class X, class F, class H>
-__global__ void __launch_bounds__(kThreads) norm_forward_kernel(const NormFwd a) {
+__global__ void __launch_bounds__(kThreads, kThreads == kMaxRowThreads ? 1 : kVec ? 3 : 4) norm_forward_kernel(const NormFwd a) {
+  constexpr int kSure = kVec ? C / 4 - 1 : 0;
   __shared__ float4 red[2][2][kMaxRowThreads / 32];
   extern __shared__ __align__(16) uint8_t norm_smem[];
   const int step = blockDim.x, D = a.D;
@@ -134,8 +131,8 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const NormFwd a)
   auto fetch = [&](int64_t row, int stage) {
     if (row < a.T) {
       uint8_t* at = norm_smem + stage * stage_bytes;
-      stage_put<false, C>(at + x_at, x_in + row * D + c0, c0, step, D);
-      if (f_in) stage_put<false, C>(at + f_at, f_in + row * D + c0, c0, step, D);
+      stage_put<kSure, C>(at + x_at, x_in + row * D + c0, c0, step, D);
+      if (f_in) stage_put<kSure, C>(at + f_at, f_in + row * D + c0, c0, step, D);
     }
     cp_async_commit();
   };
@@ -152,17 +149,17 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const NormFwd a)
       cp_async_wait<kStages - 1>();
       const uint8_t* at = norm_smem + stage * stage_bytes;
       stage = stage + 1 == kStages ? 0 : stage + 1;
-      stage_get<false, C, X>(at + x_at, c0, step, D, x);
-      if (f_in) stage_get<false, C, F>(at + f_at, c0, step, D, f);
+      stage_get<kSure, C, X>(at + x_at, c0, step, D, x);
+      if (f_in) stage_get<kSure, C, F>(at + f_at, c0, step, D, f);
     } else {
-      ld_cols<kVec>(x_in + t * D, c0, step, D, x);
-      if (f_in) ld_cols<kVec>(f_in + t * D, c0, step, D, f);
+      ld_cols<kVec, C, X, kSure>(x_in + t * D, c0, step, D, x);
+      if (f_in) ld_cols<kVec, C, F, kSure>(f_in + t * D, c0, step, D, f);
     }
     if (f_in) {
       const float g = a.gate ? a.gate[t] : 1.f;
       if (a.w_post) {
         float w[C];
-        ld_cols<kVec>(a.w_post, c0, step, D, w);
+        ld_cols<kVec, C, float, kSure>(a.w_post, c0, step, D, w);
 #pragma unroll
         for (int k = 0; k < C; ++k) s[0] = fmaf(f[k], f[k], s[0]);
         row_sums(s, red[parity][0]);
@@ -176,10 +173,10 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const NormFwd a)
 #pragma unroll
       for (int k = 0; k < C; ++k) x[k] *= a.res_scale;
     }
-    if (a.x_out) st_cols<kVec>(static_cast<X*>(a.x_out) + t * D, c0, step, D, x);
+    if (a.x_out) st_cols<kVec, C, X, kSure>(static_cast<X*>(a.x_out) + t * D, c0, step, D, x);
     if (a.h) {
       float w[C];
-      ld_cols<kVec>(a.w_pre, c0, step, D, w);
+      ld_cols<kVec, C, float, kSure>(a.w_pre, c0, step, D, w);
       s[0] = 0.f;
 #pragma unroll
       for (int k = 0; k < C; ++k) s[0] = fmaf(x[k], x[k], s[0]);
@@ -187,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const NormFwd a)
       const float r = rsqrtf(fmaf(s[0], inv_d, a.eps));
 #pragma unroll
       for (int k = 0; k < C; ++k) w[k] *= x[k] * r;
-      st_cols<kVec>(static_cast<H*>(a.h) + t * D, c0, step, D, w);
+      st_cols<kVec, C, H, kSure>(static_cast<H*>(a.h) + t * D, c0, step, D, w);
     }
   }
   if constexpr (kStages > 0) cp_async_wait<0>();
@@ -211,11 +208,11 @@ struct NormBwd {
   float* part_pre;
 };
 
-// kFull: every input but the gate is there, dx and df are wanted, and the
-// threads' columns are exactly the row's (no tests per column: backward of
-// 16384 x 2048 168 -> 130 us).
-template <bool kVec, bool kFull, int C, int kStages, int kThreads, class X, class F>
+// kAll: every input but the gate is there, and dx and df are wanted (a training
+// step's call; fewer tests).
+template <bool kVec, bool kAll, int C, int kStages, int kThreads, class X, class F>
 __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const NormBwd a) {
+  constexpr int kSure = kVec ? C / 4 - 1 : 0;
   __shared__ float4 red[2][2][kMaxRowThreads / 32];
   extern __shared__ __align__(16) uint8_t norm_smem[];
   // norm_reduce_kernel may take its place (only it: another kernel behind this
@@ -224,7 +221,7 @@ __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const NormBwd a
   const int step = blockDim.x, D = a.D;
   const int c0 = (kVec ? 4 : 1) * (int)threadIdx.x;
   const float inv_d = 1.f / (float)D;
-  const bool has_h = kFull || a.dh, has_xo = kFull || a.dx_out, has_f = kFull || a.f, post = kFull || a.w_post;
+  const bool has_h = kAll || a.dh, has_xo = kAll || a.dx_out, has_f = kAll || a.f, post = kAll || a.w_post;
   const X* x_in = static_cast<const X*>(a.x);
   const F* f_in = static_cast<const F*>(a.f);
   // a stage: dh, dx_out, x, f
@@ -238,11 +235,11 @@ __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const NormBwd a
       uint8_t* at = norm_smem + stage * stage_bytes;
       const int64_t off = row * D + c0;
       if (has_h) {
-        stage_put<kFull, C>(at + h_at, a.dh + off, c0, step, D);
-        stage_put<kFull, C>(at + x_at, x_in + off, c0, step, D);
+        stage_put<kSure, C>(at + h_at, a.dh + off, c0, step, D);
+        stage_put<kSure, C>(at + x_at, x_in + off, c0, step, D);
       }
-      if (has_xo) stage_put<kFull, C>(at + g_at, a.dx_out + off, c0, step, D);
-      if (has_f) stage_put<kFull, C>(at + f_at, f_in + off, c0, step, D);
+      if (has_xo) stage_put<kSure, C>(at + g_at, a.dx_out + off, c0, step, D);
+      if (has_f) stage_put<kSure, C>(at + f_at, f_in + off, c0, step, D);
     }
     cp_async_commit();
   };
@@ -256,7 +253,7 @@ __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const NormBwd a
   int stage = 0, parity = 0;
   for (; t < a.T; t += stride, parity ^= 1) {
     float x[C], f[C], dh[C], G[C];
-    if constexpr (!kFull) {
+    if constexpr (!kAll) {
 #pragma unroll
       for (int k = 0; k < C; ++k) x[k] = f[k] = dh[k] = G[k] = 0.f;
     }
@@ -266,24 +263,24 @@ __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const NormBwd a
       const uint8_t* at = norm_smem + stage * stage_bytes;
       stage = stage + 1 == kStages ? 0 : stage + 1;
       if (has_h) {
-        stage_get<kFull, C, float>(at + h_at, c0, step, D, dh);
-        stage_get<kFull, C, X>(at + x_at, c0, step, D, x);
+        stage_get<kSure, C, float>(at + h_at, c0, step, D, dh);
+        stage_get<kSure, C, X>(at + x_at, c0, step, D, x);
       }
-      if (has_xo) stage_get<kFull, C, float>(at + g_at, c0, step, D, G);
-      if (has_f) stage_get<kFull, C, F>(at + f_at, c0, step, D, f);
+      if (has_xo) stage_get<kSure, C, float>(at + g_at, c0, step, D, G);
+      if (has_f) stage_get<kSure, C, F>(at + f_at, c0, step, D, f);
     } else {
       if (has_h) {
-        ld_cols<kVec>(a.dh + t * D, c0, step, D, dh);
-        ld_cols<kVec>(x_in + t * D, c0, step, D, x);
+        ld_cols<kVec, C, float, kSure>(a.dh + t * D, c0, step, D, dh);
+        ld_cols<kVec, C, X, kSure>(x_in + t * D, c0, step, D, x);
       }
-      if (has_xo) ld_cols<kVec>(a.dx_out + t * D, c0, step, D, G);
-      if (has_f) ld_cols<kVec>(f_in + t * D, c0, step, D, f);
+      if (has_xo) ld_cols<kVec, C, float, kSure>(a.dx_out + t * D, c0, step, D, G);
+      if (has_f) ld_cols<kVec, C, F, kSure>(f_in + t * D, c0, step, D, f);
     }
     const float g = a.gate ? a.gate[t] : 1.f;
     float w[C];
     float s[3] = {0.f, 0.f, 0.f};
     if (has_h) {
-      ld_weights<kVec, kFull>(a.w_pre, c0, step, D, w);
+      ld_cols<kVec, C, float, kSure>(a.w_pre, c0, step, D, w);
 #pragma unroll
       for (int k = 0; k < C; ++k) {
         s[0] = fmaf(x[k], x[k], s[0]);
@@ -306,7 +303,7 @@ __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const NormBwd a
     }
     // f becomes f^ (f itself without a post-norm); dh becomes G w_post
     if (post) {
-      ld_weights<kVec, kFull>(a.w_post, c0, step, D, w);
+      ld_cols<kVec, C, float, kSure>(a.w_post, c0, step, D, w);
     } else {
 #pragma unroll
       for (int k = 0; k < C; ++k) w[k] = 1.f;
@@ -319,20 +316,20 @@ __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const NormBwd a
       dh[k] = G[k] * w[k];
       q[0] = fmaf(dh[k], f[k], q[0]);
     }
-    if (kFull || a.dx) {
+    if (kAll || a.dx) {
 #pragma unroll
       for (int k = 0; k < C; ++k) G[k] *= a.res_scale;
-      st_cols<kVec, C, float, kFull>(a.dx + t * D, c0, step, D, G);
+      st_cols<kVec, C, float, kSure>(a.dx + t * D, c0, step, D, G);
     }
     if (has_f) {
       row_sums(q, red[parity][1]);
       if (a.dgate && threadIdx.x == 0) a.dgate[t] = q[0];
     }
-    if (kFull || a.df) {
+    if (kAll || a.df) {
       const float cf = post ? -(q[0] * inv_d) : 0.f, gr = g * rf;
 #pragma unroll
       for (int k = 0; k < C; ++k) dh[k] = gr * fmaf(cf, f[k], dh[k]);
-      st_cols<kVec, C, float, kFull>(a.df + t * D, c0, step, D, dh);
+      st_cols<kVec, C, float, kSure>(a.df + t * D, c0, step, D, dh);
     }
   }
   if constexpr (kStages > 0) cp_async_wait<0>();
@@ -374,21 +371,27 @@ __global__ void __launch_bounds__(kReduceUnits* kReduceRows)
   if (lane == 0 && blockIdx.x * kCols + warp < D) dw[blockIdx.x * kCols + warp] += sum;
 }
 
-// The kernels' forms, by columns per thread.  Vector rows: staged, 8 columns
-// while a warp has a row's worth and 16 beyond (the sums over the threads then
-// cost half the instructions per column: forward of 16384 x 2048 78.7 -> 76.2
-// us), up to 4096 columns, where two rows of the widest types fit shared
-// memory; beyond, straight into registers.  Rows of other widths or alignment:
-// 4 columns a thread (their loads are single elements: more threads), 16 where
-// 512 threads of 4 are not enough.
-enum class Form { kStaged8, kStaged16, kVector, kScalar, kScalarWide };
-Form row_form(bool vec, int64_t D) {
-  if (!vec) return D <= 4 * kMaxRowThreads ? Form::kScalar : Form::kScalarWide;
-  return D <= 256 ? Form::kStaged8 : D <= 16 * kRowThreads ? Form::kStaged16 : Form::kVector;
+// A row's threads, a multiple of 32, and columns per thread.  Vector rows: as few
+// threads as have the row in 4 units of 4 columns (the sums over the threads then
+// cost the fewest instructions per column: at 2048 columns 2 units 78.7 us
+// forward, 4 units 76.2), and as few units as these need: every unit but the last
+// is whole for all threads and needs no tests (backward of 16384 x 2048 with
+// tests 168 us, without 130).  Rows of other widths or alignment, whose loads are
+// single elements, are bound by latency: 4 columns a thread (backward of 6946 x
+// 1911 bf16 with 4 100 us, with 8 122; forward of 60000 x 301 70 and 80), the
+// forward of over 512 columns 8 with 4 CTAs on an SM (6946 x 1911 46 us, with 4
+// 62), rows of over 2048 columns 16.
+struct RowPlan {
+  int threads, cols;
+};
+RowPlan row_plan(bool vec, bool forward, int64_t D) {
+  if (!vec) {
+    const int cols = D > 4 * kMaxRowThreads ? 16 : forward && D > 512 ? 8 : 4;
+    return {(int)(((D + cols - 1) / cols + 31) / 32 * 32), cols};
+  }
+  const int threads = (int)((D + 511) / 512 * 32);
+  return {threads, (int)((D + 4 * threads - 1) / (4 * threads)) * 4};
 }
-
-// A row's threads: a multiple of 32.
-int row_threads(int64_t D, int cols) { return (int)(((D + cols - 1) / cols + 31) / 32 * 32); }
 
 // The backward's CTAs, each with a row of partial sums: up to 1024 threads on
 // each of 148 SMs, and no more than 16 CTAs there.
@@ -409,9 +412,8 @@ cudaError_t resident_ctas(K kern, int threads, size_t smem, int n_sm, int64_t mo
 }
 
 template <bool kVec, int C, int kStages, int kThreads, class X, class F, class H>
-cudaError_t forward_launch(const NormFwd& a, int n_sm, cudaStream_t stream) {
+cudaError_t forward_launch(const NormFwd& a, int threads, int n_sm, cudaStream_t stream) {
   auto kern = norm_forward_kernel<kVec, C, kStages, kThreads, X, F, H>;
-  const int threads = row_threads(a.D, C);
   const size_t smem = (size_t)kStages * threads * C * (sizeof(X) + sizeof(F));
   unsigned grid = 0;
   const cudaError_t e = resident_ctas(kern, threads, smem, n_sm, a.T, &grid);
@@ -421,29 +423,34 @@ cudaError_t forward_launch(const NormFwd& a, int n_sm, cudaStream_t stream) {
 }
 
 template <class X, class F, class H>
-cudaError_t forward_form(const NormFwd& a, Form form, int n_sm, cudaStream_t stream) {
-  switch (form) {
-    case Form::kStaged8: return forward_launch<true, 8, kStages, kRowThreads, X, F, H>(a, n_sm, stream);
-    case Form::kStaged16: return forward_launch<true, 16, kStages, kRowThreads, X, F, H>(a, n_sm, stream);
-    case Form::kVector: return forward_launch<true, 16, 0, kMaxRowThreads, X, F, H>(a, n_sm, stream);
-    case Form::kScalar: return forward_launch<false, 4, 0, kMaxRowThreads, X, F, H>(a, n_sm, stream);
-    default: return forward_launch<false, 16, 0, kMaxRowThreads, X, F, H>(a, n_sm, stream);
+cudaError_t forward_form(const NormFwd& a, bool vec, int n_sm, cudaStream_t stream) {
+  const RowPlan p = row_plan(vec, true, a.D);
+  if (!vec)
+    return p.cols == 4   ? forward_launch<false, 4, 0, kRowThreads, X, F, H>(a, p.threads, n_sm, stream)
+           : p.cols == 8 ? forward_launch<false, 8, 0, kRowThreads, X, F, H>(a, p.threads, n_sm, stream)
+                         : forward_launch<false, 16, 0, kMaxRowThreads, X, F, H>(a, p.threads, n_sm, stream);
+  if (p.threads > kRowThreads)
+    return forward_launch<true, 16, kStages, kMaxRowThreads, X, F, H>(a, p.threads, n_sm, stream);
+  switch (p.cols) {
+    case 4: return forward_launch<true, 4, kStages, kRowThreads, X, F, H>(a, p.threads, n_sm, stream);
+    case 8: return forward_launch<true, 8, kStages, kRowThreads, X, F, H>(a, p.threads, n_sm, stream);
+    case 12: return forward_launch<true, 12, kStages, kRowThreads, X, F, H>(a, p.threads, n_sm, stream);
+    default: return forward_launch<true, 16, kStages + 1, kRowThreads, X, F, H>(a, p.threads, n_sm, stream);
   }
 }
 
 template <class X>
-cudaError_t forward_types(const NormFwd& a, bool f_bf16, bool h_bf16, Form form, int n_sm, cudaStream_t stream) {
+cudaError_t forward_types(const NormFwd& a, bool f_bf16, bool h_bf16, bool vec, int n_sm, cudaStream_t stream) {
   if (f_bf16)
-    return h_bf16 ? forward_form<X, uint16_t, uint16_t>(a, form, n_sm, stream)
-                  : forward_form<X, uint16_t, float>(a, form, n_sm, stream);
-  return h_bf16 ? forward_form<X, float, uint16_t>(a, form, n_sm, stream)
-                : forward_form<X, float, float>(a, form, n_sm, stream);
+    return h_bf16 ? forward_form<X, uint16_t, uint16_t>(a, vec, n_sm, stream)
+                  : forward_form<X, uint16_t, float>(a, vec, n_sm, stream);
+  return h_bf16 ? forward_form<X, float, uint16_t>(a, vec, n_sm, stream)
+                : forward_form<X, float, float>(a, vec, n_sm, stream);
 }
 
-template <bool kVec, bool kFull, int C, int kStages, int kThreads, class X, class F>
-cudaError_t backward_launch(const NormBwd& a, int n_sm, int* ctas, cudaStream_t stream) {
-  auto kern = norm_backward_kernel<kVec, kFull, C, kStages, kThreads, X, F>;
-  const int threads = row_threads(a.D, C);
+template <bool kVec, bool kAll, int C, int kStages, int kThreads, class X, class F>
+cudaError_t backward_launch(const NormBwd& a, int threads, int n_sm, int* ctas, cudaStream_t stream) {
+  auto kern = norm_backward_kernel<kVec, kAll, C, kStages, kThreads, X, F>;
   const size_t smem = (size_t)kStages * threads * C * (8 + sizeof(X) + sizeof(F));
   unsigned grid = 0;
   const cudaError_t e =
@@ -454,18 +461,31 @@ cudaError_t backward_launch(const NormBwd& a, int n_sm, int* ctas, cudaStream_t 
   return cudaGetLastError();
 }
 
-template <class X, class F>
-cudaError_t backward_form(const NormBwd& a, Form form, int n_sm, int* ctas, cudaStream_t stream) {
-  const bool full = a.dh && a.dx_out && a.f && a.w_post && a.dx && a.df && a.D % (16 * 32) == 0;
-  switch (form) {
-    case Form::kStaged8: return backward_launch<true, false, 8, kStages, kRowThreads, X, F>(a, n_sm, ctas, stream);
-    case Form::kStaged16:
-      return full ? backward_launch<true, true, 16, kStages, kRowThreads, X, F>(a, n_sm, ctas, stream)
-                  : backward_launch<true, false, 16, kStages, kRowThreads, X, F>(a, n_sm, ctas, stream);
-    case Form::kVector: return backward_launch<true, false, 16, 0, kMaxRowThreads, X, F>(a, n_sm, ctas, stream);
-    case Form::kScalar: return backward_launch<false, false, 4, 0, kMaxRowThreads, X, F>(a, n_sm, ctas, stream);
-    default: return backward_launch<false, false, 16, 0, kMaxRowThreads, X, F>(a, n_sm, ctas, stream);
+size_t stage_bytes(const RowPlan& p, size_t x, size_t f) { return (size_t)kStages * p.threads * p.cols * (8 + x + f); }
+
+template <bool kAll, class X, class F>
+cudaError_t backward_staged(const NormBwd& a, const RowPlan& p, int n_sm, int* ctas, cudaStream_t stream) {
+  switch (p.cols) {
+    case 4: return backward_launch<true, kAll, 4, kStages, kRowThreads, X, F>(a, p.threads, n_sm, ctas, stream);
+    case 8: return backward_launch<true, kAll, 8, kStages, kRowThreads, X, F>(a, p.threads, n_sm, ctas, stream);
+    case 12: return backward_launch<true, kAll, 12, kStages, kRowThreads, X, F>(a, p.threads, n_sm, ctas, stream);
+    default: return backward_launch<true, kAll, 16, kStages, kRowThreads, X, F>(a, p.threads, n_sm, ctas, stream);
   }
+}
+
+template <class X, class F>
+cudaError_t backward_form(const NormBwd& a, bool vec, int n_sm, int* ctas, cudaStream_t stream) {
+  const RowPlan p = row_plan(vec, false, a.D);
+  if (!vec)
+    return p.cols == 4
+               ? backward_launch<false, false, 4, 0, kMaxRowThreads, X, F>(a, p.threads, n_sm, ctas, stream)
+               : backward_launch<false, false, 16, 0, kMaxRowThreads, X, F>(a, p.threads, n_sm, ctas, stream);
+  if (p.threads > kRowThreads)  // (of more than 7040 columns, two fp32 rows do not fit shared memory)
+    return stage_bytes(p, sizeof(X), sizeof(F)) <= kMaxSmem
+               ? backward_launch<true, false, 16, kStages, kMaxRowThreads, X, F>(a, p.threads, n_sm, ctas, stream)
+               : backward_launch<true, false, 16, 0, kMaxRowThreads, X, F>(a, p.threads, n_sm, ctas, stream);
+  return a.dh && a.dx_out && a.f && a.w_post && a.dx && a.df ? backward_staged<true, X, F>(a, p, n_sm, ctas, stream)
+                                                             : backward_staged<false, X, F>(a, p, n_sm, ctas, stream);
 }
 
 bool valid(mole_dtype dt) { return dt == MOLE_F32 || dt == MOLE_BF16; }
@@ -474,7 +494,7 @@ size_t size_of(mole_dtype dt) { return dt == MOLE_BF16 ? 2 : 4; }
 // Rows of partial sums of each weight gradient, 16-byte aligned.
 int64_t part_ld(int64_t D) { return (D + 3) / 4 * 4; }
 size_t partial_bytes(int64_t T, int64_t D) {
-  const int64_t rows = std::min<int64_t>(T, max_backward_ctas(row_threads(D, 16)));  // 16: the fewest threads
+  const int64_t rows = std::min<int64_t>(T, max_backward_ctas(row_plan(true, false, D).threads));  // the fewest threads
   return ((size_t)rows * (size_t)part_ld(D) * 4 + 255) / 256 * 256;
 }
 
@@ -501,10 +521,9 @@ extern "C" mole_status mole_block_norm_forward(const void* x, mole_dtype dt_x, c
                    aligned_rows(x_out, dt_x == MOLE_BF16) && aligned_rows(h, dt_h == MOLE_BF16) &&
                    aligned16(w_post) && aligned16(w_pre);
   const NormFwd a{x, f, w_post, gate, w_pre, res_scale, eps, T, (int)D, x_out, h};
-  const Form form = row_form(vec, D);
   const bool fb = dt_f == MOLE_BF16, hb = dt_h == MOLE_BF16;
-  return cuda_status(dt_x == MOLE_BF16 ? forward_types<uint16_t>(a, fb, hb, form, n_sm, stream)
-                                       : forward_types<float>(a, fb, hb, form, n_sm, stream));
+  return cuda_status(dt_x == MOLE_BF16 ? forward_types<uint16_t>(a, fb, hb, vec, n_sm, stream)
+                                       : forward_types<float>(a, fb, hb, vec, n_sm, stream));
 }
 
 extern "C" size_t mole_block_norm_backward_workspace(int64_t T, int64_t D) {
@@ -549,15 +568,14 @@ extern "C" mole_status mole_block_norm_backward(const void* x_out, mole_dtype dt
                    aligned16(df);
   const NormBwd a{x_out, f,  w_post, gate, w_pre, res_scale, eps,       T, (int)D,
                   dx_out, dh, dx,     df,   dgate, part_post, part_pre};
-  const Form form = row_form(vec, D);
   int ctas = 0;
   cudaError_t e;
   if (dt_x == MOLE_BF16)
-    e = dt_f == MOLE_BF16 ? backward_form<uint16_t, uint16_t>(a, form, n_sm, &ctas, stream)
-                          : backward_form<uint16_t, float>(a, form, n_sm, &ctas, stream);
+    e = dt_f == MOLE_BF16 ? backward_form<uint16_t, uint16_t>(a, vec, n_sm, &ctas, stream)
+                          : backward_form<uint16_t, float>(a, vec, n_sm, &ctas, stream);
   else
-    e = dt_f == MOLE_BF16 ? backward_form<float, uint16_t>(a, form, n_sm, &ctas, stream)
-                          : backward_form<float, float>(a, form, n_sm, &ctas, stream);
+    e = dt_f == MOLE_BF16 ? backward_form<float, uint16_t>(a, vec, n_sm, &ctas, stream)
+                          : backward_form<float, float>(a, vec, n_sm, &ctas, stream);
   if (e != cudaSuccess) return MOLE_ERR_CUDA;
   if (part_pre || part_post) {
     cudaLaunchConfig_t cfg = {};

@@ -48,14 +48,14 @@ __device__ __forceinline__ void st_unit(uint16_t* p, float a, float b, float c, 
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(a, b), pack_bf16(c, d));
 }
 
-// (kAll: all of the thread's columns lie in the row.)
-template <bool kVec, int C, class T, bool kAll = false>
+// (kSure: how many of the thread's first units lie in the row for every thread.)
+template <bool kVec, int C, class T, int kSure = 0>
 __device__ __forceinline__ void ld_cols(const T* row, int col0, int step, int D, float (&f)[C]) {
   if constexpr (kVec) {
 #pragma unroll
     for (int u = 0; u < C / 4; ++u) {
       float x[4] = {0.f, 0.f, 0.f, 0.f};
-      if (kAll || col0 + 4 * u * step < D) ld_unit(row + col0 + 4 * u * step, x);
+      if (u < kSure || col0 + 4 * u * step < D) ld_unit(row + col0 + 4 * u * step, x);
 #pragma unroll
       for (int k = 0; k < 4; ++k) f[4 * u + k] = x[k];
     }
@@ -64,12 +64,12 @@ __device__ __forceinline__ void ld_cols(const T* row, int col0, int step, int D,
     for (int k = 0; k < C; ++k) f[k] = col0 + k * step < D ? ld1(row + col0 + k * step) : 0.f;
   }
 }
-template <bool kVec, int C, class T, bool kAll = false>
+template <bool kVec, int C, class T, int kSure = 0>
 __device__ __forceinline__ void st_cols(T* row, int col0, int step, int D, const float (&f)[C]) {
   if constexpr (kVec) {
 #pragma unroll
     for (int u = 0; u < C / 4; ++u)
-      if (kAll || col0 + 4 * u * step < D)
+      if (u < kSure || col0 + 4 * u * step < D)
         st_unit(row + col0 + 4 * u * step, f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3]);
   } else {
 #pragma unroll
@@ -150,11 +150,12 @@ RowSplit row_split(int64_t D, int unit, int max_tx) {
   return {tx, (int)((units + tx - 1) / tx)};
 }
 
-// Lets `kern` have up to 220 KB of dynamic shared memory: always the same
+// Lets `kern` have up to kMaxSmem of dynamic shared memory: always the same
 // number, so that calls from several host threads do not lower each other's.
+constexpr size_t kMaxSmem = 220 * 1024;
 template <class K>
 cudaError_t allow_smem(K kern) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
 }
 
 // Whether vector accesses (units of 4 columns) can start at p.

@@ -40,7 +40,7 @@ def _check_forward(mole, x, f, w_post, gate, res_scale, w_pre, th, in_place=Fals
 
 @pytest.mark.parametrize("tx,tf,th", [(F32, F32, BF16), (BF16, BF16, BF16), (F32, BF16, F32), (BF16, F32, F32)])
 @pytest.mark.parametrize("T,D", [(1, 1), (1, 2048), (3, 7), (9, 64), (10, 20), (130, 256), (65, 264), (37, 1001), (20, 2056),
-                                 (11, 4097), (6, 8192), (2000, 128), (5000, 512), (41, 2048)])
+                                 (11, 4097), (6, 8192), (2000, 128), (5000, 512), (41, 2048), (300, 384), (200, 768), (70, 1576), (8, 4100), (9, 3001), (300, 301), (6, 7680)])
 def test_forward(mole, T, D, tx, tf, th):
     rng = np.random.default_rng(T + D)
     _check_forward(mole, *_layer(rng, T, D, tx, tf)[:4], 0.8, _rand(rng, D), th)
@@ -117,7 +117,7 @@ def _check_backward(mole, x, f, w_post, gate, res_scale, w_pre, dx_out, dh, alia
 
 @pytest.mark.parametrize("tx,tf", [(F32, F32), (BF16, BF16), (F32, BF16), (BF16, F32)])
 @pytest.mark.parametrize("T,D", [(1, 1), (1, 2048), (3, 7), (9, 64), (10, 20), (130, 256), (65, 264), (37, 1001), (20, 2056),
-                                 (11, 4097), (6, 8192), (3000, 128), (5001, 72), (700, 512), (41, 2048), (9, 4096)])
+                                 (11, 4097), (6, 8192), (3000, 128), (5001, 72), (700, 512), (41, 2048), (9, 4096), (300, 384), (200, 768), (70, 1576), (8, 4100), (9, 3001), (300, 301), (6, 7680)])
 def test_backward(mole, T, D, tx, tf):
     rng = np.random.default_rng(T + D)
     x, f, w_post, g, w_pre = _layer(rng, T, D, tx, tf)
