@@ -28,13 +28,13 @@ namespace mole {
 namespace {
 
 constexpr int kAdamThreads = 256;
-constexpr int kAdamUnits = 2;                               // units of 4 elements a thread
+constexpr int kAdamUnits = 2;                              // units of 4 elements a thread
 constexpr int kAdamChunk = 4 * kAdamUnits * kAdamThreads;  // elements a CTA
-constexpr int kAdamBlock = 128;                       // elements per scale
-constexpr int kAdamTensors = 128;                         // per launch (10 KB of parameters)
+constexpr int kAdamBlock = 128;                            // elements per scale
+constexpr int kAdamTensors = 128;                          // per launch (10 KB of parameters)
 constexpr float kInvE4m3Max = (float)(1.0 / 448.0);
-constexpr float kScaleFloor = 0x1p-120f;              // its reciprocal is finite
-constexpr float kE4m3Tiny = 0x1p-9f;                  // the smallest nonzero code
+constexpr float kScaleFloor = 0x1p-120f;                   // its reciprocal is finite
+constexpr float kE4m3Tiny = 0x1p-9f;                       // the smallest nonzero code
 
 struct AdamTensor {
   void* param;

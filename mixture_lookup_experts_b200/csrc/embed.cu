@@ -11,7 +11,8 @@
 //   1. embed_sort_kernel: (id, t) sorted by id, stably (ascending t inside an
 //      id), by a radix sort of 8-bit digits run by ONE cluster of 16 CTAs: the
 //      digit counts of its 512 warps meet in distributed shared memory, so a
-//      pass costs two cluster barriers instead of two kernel boundaries.
+//      pass costs two cluster barriers instead of two kernel boundaries (up to
+//      kOneCtaTokens by one CTA).
 //   2. embed_chunk_kernel: fixed chunks of the sorted order, one group of
 //      threads per (chunk, slice of columns); the runs of equal ids go to dE,
 //      but those longer than a chunk leave partial sums.
@@ -39,6 +40,7 @@ constexpr int kJoinThreads = 256;
 constexpr int kChunkUnits = 2, kChunkSlots = 5, kScalarCols = 4;
 constexpr int64_t kChunkGroups = 1776;  // chunks times slices: 12 CTAs for each of 148 SMs
 constexpr int kSmallTokens = 1024;
+constexpr int kOneCtaTokens = 2048;
 
 // ---- forward ----
 // blockDim = (tx, 256 / tx): a row slice per group of tx threads, kRows rows in
@@ -180,6 +182,56 @@ __device__ __forceinline__ void scan_digits(SortSmem& s, int all, int before) {
     s.base[threadIdx.x] = off;
   }
   __syncthreads();
+}
+
+// The sort by one CTA of up to 32 * H * kSortWarps tokens, in its shared memory:
+// `sorted` has the result.
+template <int H>
+__device__ __forceinline__ void cta_sort(SortSmem& s, const int32_t* ids, int T, int64_t V, int passes, int2* sorted,
+                                         unsigned* err) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lo = 32 * H * warp;
+  int2 e[H];
+  int rank[H];
+#pragma unroll
+  for (int j = 0; j < H; ++j) {
+    const int i = lo + 32 * j + lane;
+    if (i < T) {
+      e[j] = sort_key(ids, V, i);
+      if (blockIdx.x == 0 && (int64_t)e[j].x == V) atomicOr(err, kErrIndex);
+    }
+  }
+  for (int pass = 0; pass < passes; ++pass) {
+    for (int d = lane; d < kDigits; d += 32) s.hist[warp][d] = 0;
+    __syncwarp();
+    rank_tiles<H>(e, rank, T - lo, 8 * pass, s.hist[warp]);
+    __syncthreads();
+    scan_digits(s, scan_warps(s), 0);
+#pragma unroll
+    for (int j = 0; j < H; ++j)
+      if (lo + 32 * j + lane < T) {
+        const int d = ((unsigned)e[j].x >> (8 * pass)) & (kDigits - 1);
+        sorted[s.base[d] + s.hist[warp][d] + rank[j]] = e[j];
+      }
+    __syncthreads();
+    if (pass + 1 < passes) {
+#pragma unroll
+      for (int j = 0; j < H; ++j)
+        if (lo + 32 * j + lane < T) e[j] = sorted[lo + 32 * j + lane];
+    }
+  }
+}
+
+// Up to kOneCtaTokens tokens: one CTA, no cluster barriers (the gradient of 1500
+// tokens of 2048 16.2 us, by the cluster 18.5; of 4096 of 512 18.4 and 16.4).
+__global__ void __launch_bounds__(kSortThreads, 1) embed_sort_one_kernel(const SortArgs a) {
+  extern __shared__ __align__(16) uint8_t sort_smem[];
+  SortSmem& s = *reinterpret_cast<SortSmem*>(sort_smem);
+  int2* sorted = reinterpret_cast<int2*>(sort_smem + sizeof(SortSmem));  // [kOneCtaTokens]
+  pdl_trigger();  // the chunk kernel may take its place on the other SMs
+  if (threadIdx.x == 0) *a.n_runs = 0;
+  cta_sort<kOneCtaTokens / kSortThreads>(s, a.ids, (int)a.T, a.V, a.passes, sorted, a.err);
+  for (int i = threadIdx.x; i < (int)a.T; i += kSortThreads) a.to[i] = sorted[i];
 }
 
 // Where the sort's elements live between passes: while a CTA's share fits its
@@ -589,42 +641,13 @@ template <class In>
 __global__ void __launch_bounds__(kSortThreads, 1)
     embed_small_kernel(const int32_t* __restrict__ ids, int T, int64_t V, int passes, const In* __restrict__ dout,
                        int D, float scale, float* dE, unsigned* err) {
-  constexpr int H = kSmallTokens / kSortThreads, kQ = 8;
+  constexpr int kQ = 8;
   extern __shared__ __align__(16) uint8_t sort_smem[];
   SortSmem& s = *reinterpret_cast<SortSmem*>(sort_smem);
   int2* sorted = reinterpret_cast<int2*>(sort_smem + sizeof(SortSmem));  // [kSmallTokens]
   float* part = reinterpret_cast<float*>(sorted + kSmallTokens);         // [kSortWarps][2][32]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int lo = 32 * H * warp;
-  int2 e[H];
-  int rank[H];
-#pragma unroll
-  for (int j = 0; j < H; ++j) {
-    const int i = lo + 32 * j + lane;
-    if (i < T) {
-      e[j] = sort_key(ids, V, i);
-      if (blockIdx.x == 0 && (int64_t)e[j].x == V) atomicOr(err, kErrIndex);
-    }
-  }
-  for (int pass = 0; pass < passes; ++pass) {
-    for (int d = lane; d < kDigits; d += 32) s.hist[warp][d] = 0;
-    __syncwarp();
-    rank_tiles<H>(e, rank, T - lo, 8 * pass, s.hist[warp]);
-    __syncthreads();
-    scan_digits(s, scan_warps(s), 0);
-#pragma unroll
-    for (int j = 0; j < H; ++j)
-      if (lo + 32 * j + lane < T) {
-        const int d = ((unsigned)e[j].x >> (8 * pass)) & (kDigits - 1);
-        sorted[s.base[d] + s.hist[warp][d] + rank[j]] = e[j];
-      }
-    __syncthreads();
-    if (pass + 1 < passes) {
-#pragma unroll
-      for (int j = 0; j < H; ++j)
-        if (lo + 32 * j + lane < T) e[j] = sorted[lo + 32 * j + lane];
-    }
-  }
+  cta_sort<kSmallTokens / kSortThreads>(s, ids, T, V, passes, sorted, err);
   const int col = blockIdx.x * 32 + lane;
   auto begin = [&](int w) { return (int)((int64_t)T * w / kSortWarps); };
   const int p0 = begin(warp), p1 = begin(warp + 1);
@@ -739,6 +762,13 @@ cudaError_t launch_sort(const SortArgs& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+cudaError_t launch_sort_one(const SortArgs& a, cudaStream_t stream) {
+  const cudaError_t e = allow_smem(embed_sort_one_kernel);
+  if (e != cudaSuccess) return e;
+  embed_sort_one_kernel<<<1, kSortThreads, sizeof(SortSmem) + kOneCtaTokens * sizeof(int2), stream>>>(a);
+  return cudaGetLastError();
+}
+
 template <class In>
 cudaError_t launch_small(const int32_t* ids, int64_t T, int64_t V, int passes, const void* dout, int D, float scale,
                          float* dE, unsigned* err, cudaStream_t stream) {
@@ -805,7 +835,9 @@ mole_status embed_backward(const int32_t* ids, int64_t T, const void* dout, bool
     return cuda_status((bf16 ? launch_small<uint16_t> : launch_small<float>)(ids, T, V, passes, dout, (int)D, scale, dE,
                                                                             err, stream));
   const SortArgs sa{ids, T, V, w.buf[0], w.buf[1], passes, w.n_runs, err};
-  if (T <= kSortCtas * kSortThreads)
+  if (T <= kOneCtaTokens)
+    e = launch_sort_one(sa, stream);
+  else if (T <= kSortCtas * kSortThreads)
     e = launch_sort<1>(sa, stream);
   else if (T <= 4 * kSortCtas * kSortThreads)
     e = launch_sort<4>(sa, stream);

@@ -105,7 +105,7 @@ def test_backward(mole, T, V, D, kind, dtype):
     _check_backward(mole, rng, T, V, D, dtype, inputs.draw_ids(rng, T, V, kind))
 
 
-@pytest.mark.parametrize("T", [1, 15, 16, 17, 32, 33, 1024, 1025, 4096, 40000])
+@pytest.mark.parametrize("T", [1, 15, 16, 17, 32, 33, 1024, 1025, 2048, 2049, 4096, 40000])
 def test_backward_one_id(mole, T):
     # all tokens one id: a single run over every chunk
     rng = np.random.default_rng(T)
