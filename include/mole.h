@@ -435,9 +435,10 @@ mole_status mole_embed_backward(const int32_t* ids, int64_t T, const void* dout,
  * dw_post only; calls that share one must not overlap on the GPU.
  *
  * Both take any D up to 8192 and T up to 2^31 - 1 (T == 0 is a no-op), and
- * pointers aligned to their element; rows that start on 4 elements (D a
- * multiple of 4, pointers aligned to 16 bytes, bf16 ones to 8) take the vector
- * kernels.
+ * pointers aligned to their element; where all pointers to rows and weights are
+ * aligned to 16 bytes (bf16 ones to 8) the rows take vector accesses, of any D
+ * as long as two of them fit shared memory (fp32 backward: up to 5632 columns
+ * where D is not a multiple of 4).
  */
 mole_status mole_block_norm_forward(const void* x, mole_dtype dt_x, const void* f, mole_dtype dt_f,
                                     const float* w_post, const float* gate, float res_scale, const float* w_pre,
@@ -477,8 +478,8 @@ mole_status mole_block_norm_backward(const void* x_out, mole_dtype dt_x, const v
  * tensors and config are HOST structs, read before the call returns.  No
  * memory that a call writes may overlap anything else in its list
  * (MOLE_ERR_ARG).  Any n >= 0 and pointers aligned to their element; a
- * tensor whose pointers are all aligned to 4 elements takes vector accesses.  One launch per
- * 128 tensors.
+ * tensor whose pointers are all aligned to 4 elements takes vector accesses.
+ * One launch per 128 tensors.
  */
 typedef struct {
   void* param;         /* [n] dt_param, overwritten */

@@ -27,6 +27,7 @@ namespace {
 constexpr int kRowThreads = 256, kMaxRowThreads = 512;  // a row's threads, up to 4096 columns and beyond
 constexpr int64_t kMaxNormD = 16 * kMaxRowThreads;
 constexpr int kStages = 2;
+constexpr int64_t kFewRows = 148 * 16;
 constexpr int kReduceUnits = 8, kReduceRows = 128;  // 32 columns and 32 warps a CTA
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -74,23 +75,101 @@ __device__ __forceinline__ void row_sums(float (&v)[K], float4* red) {
   }
 }
 
+// How the threads have a row's columns: as single elements, or in units of 4
+// with vector accesses (rows.cuh).  kUnits: every row starts on a unit (D a
+// multiple of 4).  kShifted: the tensors do but not every row: units are those
+// of the memory, the first one of a row begins up to 3 columns before it, and
+// the last one ends behind it.  The shift is (t D) mod 4, so a CTA whose rows
+// are a multiple of 4 apart has one shift, and a thread the same columns, for
+// all of them.
+enum Form { kElements, kShifted, kUnits };
+
+// The CTA's shift.
+template <Form kForm>
+__device__ __forceinline__ int first_column(int D) {
+  if (kForm == kElements) return (int)threadIdx.x;
+  return 4 * (int)threadIdx.x - (kForm == kShifted ? (int)(((int64_t)blockIdx.x * D) & 3) : 0);
+}
+
 // A thread's columns of a row on their way through shared memory (cp.async;
 // each thread reads back its own copies only).  at: the thread's place in the
-// stage's area of this tensor, which lies there as in the row.
-template <int kSure, int C, class T>
+// stage's area of this tensor, which lies there as in the row; row: the row's
+// first element.  What lies behind the row is neither read nor left to chance (0);
+// what lies before it is the end of the row before, left out by stage_get.
+template <Form kForm, int kSure, int C, class T>
 __device__ __forceinline__ void stage_put(uint8_t* at, const T* row, int col0, int step, int D) {
 #pragma unroll
-  for (int u = 0; u < C / 4; ++u)
-    if (u < kSure || col0 + 4 * u * step < D) cp_async<4 * sizeof(T)>(at + u * step * 4 * sizeof(T), row + 4 * u * step);
+  for (int u = 0; u < C / 4; ++u) {
+    const int col = col0 + 4 * u * step;
+    if (u < kSure)
+      cp_async<4 * sizeof(T)>(at + u * step * 4 * sizeof(T), row + col);
+    else if (col < D)
+      cp_async<4 * sizeof(T), kForm == kShifted>(at + u * step * 4 * sizeof(T), row + col,
+                                                 (int)sizeof(T) * std::min(4, D - col));
+  }
 }
-template <int kSure, int C, class T>
+template <Form kForm, int kSure, int C, class T>
 __device__ __forceinline__ void stage_get(const uint8_t* at, int col0, int step, int D, float (&f)[C]) {
 #pragma unroll
   for (int u = 0; u < C / 4; ++u) {
     float x[4] = {0.f, 0.f, 0.f, 0.f};
     if (u < kSure || col0 + 4 * u * step < D) ld_unit(reinterpret_cast<const T*>(at + u * step * 4 * sizeof(T)), x);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) f[4 * u + k] = x[k];
+    for (int k = 0; k < 4; ++k) f[4 * u + k] = kForm == kShifted && u == 0 && col0 + k < 0 ? 0.f : x[k];
+  }
+}
+
+// A weight vector, whose units are not those of the rows where these are
+// shifted: the thread's columns then lie in shared memory (`at`), as the stages'.
+template <Form kForm, int C>
+__device__ __forceinline__ void weight_put(uint8_t* at, const float* w, int col0, int step, int D) {
+  if constexpr (kForm == kShifted) {
+    if (!w) return;
+#pragma unroll
+    for (int u = 0; u < C / 4; ++u) {
+      float x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int col = col0 + 4 * u * step + k;
+        x[k] = col >= 0 && col < D ? w[col] : 0.f;
+      }
+      st_unit(reinterpret_cast<float*>(at + u * step * 16), x[0], x[1], x[2], x[3]);
+    }
+  }
+}
+template <Form kForm, int kSure, int C>
+__device__ __forceinline__ void weight_get(const uint8_t* at, const float* w, int col0, int step, int D,
+                                           float (&f)[C]) {
+  if constexpr (kForm == kShifted) {
+#pragma unroll
+    for (int u = 0; u < C / 4; ++u) {
+      float x[4];
+      ld_unit(reinterpret_cast<const float*>(at + u * step * 16), x);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[4 * u + k] = x[k];
+    }
+  } else {
+    ld_cols<kForm == kUnits, C, float, kSure>(w, col0, step, D, f);
+  }
+}
+
+// The thread's columns to a row whose first element is at `row`.
+template <Form kForm, int kSure, int C, class T>
+__device__ __forceinline__ void store_row(T* row, int col0, int step, int D, const float (&f)[C]) {
+  if constexpr (kForm == kShifted) {
+#pragma unroll
+    for (int u = 0; u < C / 4; ++u) {
+      const int col = col0 + 4 * u * step;
+      if ((u > 0 || col >= 0) && (u < kSure || col + 4 <= D)) {
+        st_unit(row + col, f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (col + k >= 0 && col + k < D) st1(row + col + k, f[4 * u + k]);
+      }
+    }
+  } else {
+    st_cols<kForm == kUnits, C, T, kSure>(row, col0, step, D, f);
   }
 }
 
@@ -114,25 +193,30 @@ struct NormFwd {
 // have 3 stages (16384 x 2048 fp32 75 to 76 us whatever the tensors' addresses;
 // with 2, 74 to 86), fewer columns 2 (16384 x 768 32.5 us, with 3 34.2); 85
 // registers a thread leave room for 6 CTAs of 4 warps.
-template <bool kVec, int C, int kStages, int kThreads, class X, class F, class H>
-__global__ void __launch_bounds__(kThreads, kThreads == kMaxRowThreads ? 1 : kVec ? 3 : 4) norm_forward_kernel(const NormFwd a) {
-  constexpr int kSure = kVec ? C / 4 - 1 : 0;
+template <Form kForm, int C, int kStages, int kThreads, class X, class F, class H>
+__global__ void __launch_bounds__(kThreads, kThreads == kMaxRowThreads ? 1 : kForm == kElements ? 4 : 3)
+    norm_forward_kernel(const NormFwd a) {
+  constexpr int kSure = kForm != kElements ? C / 4 - 1 : 0;
+  static_assert(kForm != kShifted || kStages > 0, "shifted units only through shared memory");
   __shared__ float4 red[2][2][kMaxRowThreads / 32];
   extern __shared__ __align__(16) uint8_t norm_smem[];
   const int step = blockDim.x, D = a.D;
-  const int c0 = (kVec ? 4 : 1) * (int)threadIdx.x;
+  const int c0 = first_column<kForm>(D);
   const float inv_d = 1.f / (float)D;
   const X* x_in = static_cast<const X*>(a.x);
   const F* f_in = static_cast<const F*>(a.f);
   const int stage_bytes = step * C * (int)(sizeof(X) + sizeof(F));
-  const int x_at = c0 * (int)sizeof(X), f_at = step * C * (int)sizeof(X) + c0 * (int)sizeof(F);
+  const int at0 = 4 * (int)threadIdx.x, x_at = at0 * (int)sizeof(X),
+            f_at = step * C * (int)sizeof(X) + at0 * (int)sizeof(F);
+  [[maybe_unused]] uint8_t* post_at = norm_smem + kStages * stage_bytes + 4 * at0;  // kShifted: the weights
+  [[maybe_unused]] uint8_t* pre_at = post_at + step * C * 4;
   const int64_t stride = gridDim.x;
   int64_t t = blockIdx.x;
   auto fetch = [&](int64_t row, int stage) {
     if (row < a.T) {
       uint8_t* at = norm_smem + stage * stage_bytes;
-      stage_put<kSure, C>(at + x_at, x_in + row * D + c0, c0, step, D);
-      if (f_in) stage_put<kSure, C>(at + f_at, f_in + row * D + c0, c0, step, D);
+      stage_put<kForm, kSure, C>(at + x_at, x_in + row * D, c0, step, D);
+      if (f_in) stage_put<kForm, kSure, C>(at + f_at, f_in + row * D, c0, step, D);
     }
     cp_async_commit();
   };
@@ -140,6 +224,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == kMaxRowThreads ? 1 : kVe
 #pragma unroll
     for (int k = 0; k < kStages - 1; ++k) fetch(t + k * stride, k);
   }
+  weight_put<kForm, C>(post_at, a.w_post, c0, step, D);
+  weight_put<kForm, C>(pre_at, a.w_pre, c0, step, D);
   int stage = 0, parity = 0;
   for (; t < a.T; t += stride, parity ^= 1) {
     float x[C], f[C];
@@ -149,17 +235,17 @@ __global__ void __launch_bounds__(kThreads, kThreads == kMaxRowThreads ? 1 : kVe
       cp_async_wait<kStages - 1>();
       const uint8_t* at = norm_smem + stage * stage_bytes;
       stage = stage + 1 == kStages ? 0 : stage + 1;
-      stage_get<kSure, C, X>(at + x_at, c0, step, D, x);
-      if (f_in) stage_get<kSure, C, F>(at + f_at, c0, step, D, f);
+      stage_get<kForm, kSure, C, X>(at + x_at, c0, step, D, x);
+      if (f_in) stage_get<kForm, kSure, C, F>(at + f_at, c0, step, D, f);
     } else {
-      ld_cols<kVec, C, X, kSure>(x_in + t * D, c0, step, D, x);
-      if (f_in) ld_cols<kVec, C, F, kSure>(f_in + t * D, c0, step, D, f);
+      ld_cols<kForm == kUnits, C, X, kSure>(x_in + t * D, c0, step, D, x);
+      if (f_in) ld_cols<kForm == kUnits, C, F, kSure>(f_in + t * D, c0, step, D, f);
     }
     if (f_in) {
       const float g = a.gate ? a.gate[t] : 1.f;
       if (a.w_post) {
         float w[C];
-        ld_cols<kVec, C, float, kSure>(a.w_post, c0, step, D, w);
+        weight_get<kForm, kSure>(post_at, a.w_post, c0, step, D, w);
 #pragma unroll
         for (int k = 0; k < C; ++k) s[0] = fmaf(f[k], f[k], s[0]);
         row_sums(s, red[parity][0]);
@@ -173,10 +259,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == kMaxRowThreads ? 1 : kVe
 #pragma unroll
       for (int k = 0; k < C; ++k) x[k] *= a.res_scale;
     }
-    if (a.x_out) st_cols<kVec, C, X, kSure>(static_cast<X*>(a.x_out) + t * D, c0, step, D, x);
+    if (a.x_out) store_row<kForm, kSure>(static_cast<X*>(a.x_out) + t * D, c0, step, D, x);
     if (a.h) {
       float w[C];
-      ld_cols<kVec, C, float, kSure>(a.w_pre, c0, step, D, w);
+      weight_get<kForm, kSure>(pre_at, a.w_pre, c0, step, D, w);
       s[0] = 0.f;
 #pragma unroll
       for (int k = 0; k < C; ++k) s[0] = fmaf(x[k], x[k], s[0]);
@@ -184,10 +270,27 @@ __global__ void __launch_bounds__(kThreads, kThreads == kMaxRowThreads ? 1 : kVe
       const float r = rsqrtf(fmaf(s[0], inv_d, a.eps));
 #pragma unroll
       for (int k = 0; k < C; ++k) w[k] *= x[k] * r;
-      st_cols<kVec, C, H, kSure>(static_cast<H*>(a.h) + t * D, c0, step, D, w);
+      store_row<kForm, kSure>(static_cast<H*>(a.h) + t * D, c0, step, D, w);
     }
   }
   if constexpr (kStages > 0) cp_async_wait<0>();
+}
+
+// The CTA's sums to its row of the partial ones (if there are such), each of
+// which starts on a unit: shifted columns go there one by one.
+template <Form kForm, int C>
+__device__ __forceinline__ void store_part(float* part, int col0, int step, int D, const float (&f)[C]) {
+  if (!part) return;
+  float* row = part + (int64_t)blockIdx.x * ((D + 3) & ~3);
+  if constexpr (kForm == kShifted) {
+#pragma unroll
+    for (int k = 0; k < C; ++k) {
+      const int col = col0 + 4 * (k / 4) * step + k % 4;
+      if (col >= 0 && col < D) row[col] = f[k];
+    }
+  } else {
+    st_cols<kForm == kUnits>(row, col0, step, D, f);
+  }
 }
 
 struct NormBwd {
@@ -210,36 +313,40 @@ struct NormBwd {
 
 // kAll: every input but the gate is there, and dx and df are wanted (a training
 // step's call; fewer tests).
-template <bool kVec, bool kAll, int C, int kStages, int kThreads, class X, class F>
+template <Form kForm, bool kAll, int C, int kStages, int kThreads, class X, class F>
 __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const NormBwd a) {
-  constexpr int kSure = kVec ? C / 4 - 1 : 0;
+  constexpr int kSure = kForm != kElements ? C / 4 - 1 : 0;
+  static_assert(kForm != kShifted || kStages > 0, "shifted units only through shared memory");
   __shared__ float4 red[2][2][kMaxRowThreads / 32];
   extern __shared__ __align__(16) uint8_t norm_smem[];
   // norm_reduce_kernel may take its place (only it: another kernel behind this
   // one might not wait for it)
   if (a.part_pre || a.part_post) pdl_trigger();
   const int step = blockDim.x, D = a.D;
-  const int c0 = (kVec ? 4 : 1) * (int)threadIdx.x;
+  const int c0 = first_column<kForm>(D);
   const float inv_d = 1.f / (float)D;
   const bool has_h = kAll || a.dh, has_xo = kAll || a.dx_out, has_f = kAll || a.f, post = kAll || a.w_post;
   const X* x_in = static_cast<const X*>(a.x);
   const F* f_in = static_cast<const F*>(a.f);
   // a stage: dh, dx_out, x, f
-  const int h_at = 4 * c0, g_at = step * C * 4 + 4 * c0, x_at = step * C * 8 + c0 * (int)sizeof(X),
-            f_at = step * C * (8 + (int)sizeof(X)) + c0 * (int)sizeof(F),
+  const int at0 = 4 * (int)threadIdx.x, h_at = 4 * at0, g_at = step * C * 4 + 4 * at0,
+            x_at = step * C * 8 + at0 * (int)sizeof(X),
+            f_at = step * C * (8 + (int)sizeof(X)) + at0 * (int)sizeof(F),
             stage_bytes = step * C * (8 + (int)(sizeof(X) + sizeof(F)));
+  [[maybe_unused]] uint8_t* post_at = norm_smem + kStages * stage_bytes + 4 * at0;  // kShifted: the weights
+  [[maybe_unused]] uint8_t* pre_at = post_at + step * C * 4;
   const int64_t stride = gridDim.x;
   int64_t t = blockIdx.x;
   auto fetch = [&](int64_t row, int stage) {
     if (row < a.T) {
       uint8_t* at = norm_smem + stage * stage_bytes;
-      const int64_t off = row * D + c0;
+      const int64_t off = row * D;
       if (has_h) {
-        stage_put<kSure, C>(at + h_at, a.dh + off, c0, step, D);
-        stage_put<kSure, C>(at + x_at, x_in + off, c0, step, D);
+        stage_put<kForm, kSure, C>(at + h_at, a.dh + off, c0, step, D);
+        stage_put<kForm, kSure, C>(at + x_at, x_in + off, c0, step, D);
       }
-      if (has_xo) stage_put<kSure, C>(at + g_at, a.dx_out + off, c0, step, D);
-      if (has_f) stage_put<kSure, C>(at + f_at, f_in + off, c0, step, D);
+      if (has_xo) stage_put<kForm, kSure, C>(at + g_at, a.dx_out + off, c0, step, D);
+      if (has_f) stage_put<kForm, kSure, C>(at + f_at, f_in + off, c0, step, D);
     }
     cp_async_commit();
   };
@@ -247,6 +354,8 @@ __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const NormBwd a
 #pragma unroll
     for (int k = 0; k < kStages - 1; ++k) fetch(t + k * stride, k);
   }
+  weight_put<kForm, C>(post_at, a.w_post, c0, step, D);
+  weight_put<kForm, C>(pre_at, a.w_pre, c0, step, D);
   float acc_pre[C], acc_post[C];
 #pragma unroll
   for (int k = 0; k < C; ++k) acc_pre[k] = acc_post[k] = 0.f;
@@ -263,24 +372,24 @@ __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const NormBwd a
       const uint8_t* at = norm_smem + stage * stage_bytes;
       stage = stage + 1 == kStages ? 0 : stage + 1;
       if (has_h) {
-        stage_get<kSure, C, float>(at + h_at, c0, step, D, dh);
-        stage_get<kSure, C, X>(at + x_at, c0, step, D, x);
+        stage_get<kForm, kSure, C, float>(at + h_at, c0, step, D, dh);
+        stage_get<kForm, kSure, C, X>(at + x_at, c0, step, D, x);
       }
-      if (has_xo) stage_get<kSure, C, float>(at + g_at, c0, step, D, G);
-      if (has_f) stage_get<kSure, C, F>(at + f_at, c0, step, D, f);
+      if (has_xo) stage_get<kForm, kSure, C, float>(at + g_at, c0, step, D, G);
+      if (has_f) stage_get<kForm, kSure, C, F>(at + f_at, c0, step, D, f);
     } else {
       if (has_h) {
-        ld_cols<kVec, C, float, kSure>(a.dh + t * D, c0, step, D, dh);
-        ld_cols<kVec, C, X, kSure>(x_in + t * D, c0, step, D, x);
+        ld_cols<kForm == kUnits, C, float, kSure>(a.dh + t * D, c0, step, D, dh);
+        ld_cols<kForm == kUnits, C, X, kSure>(x_in + t * D, c0, step, D, x);
       }
-      if (has_xo) ld_cols<kVec, C, float, kSure>(a.dx_out + t * D, c0, step, D, G);
-      if (has_f) ld_cols<kVec, C, F, kSure>(f_in + t * D, c0, step, D, f);
+      if (has_xo) ld_cols<kForm == kUnits, C, float, kSure>(a.dx_out + t * D, c0, step, D, G);
+      if (has_f) ld_cols<kForm == kUnits, C, F, kSure>(f_in + t * D, c0, step, D, f);
     }
     const float g = a.gate ? a.gate[t] : 1.f;
     float w[C];
     float s[3] = {0.f, 0.f, 0.f};
     if (has_h) {
-      ld_cols<kVec, C, float, kSure>(a.w_pre, c0, step, D, w);
+      weight_get<kForm, kSure>(pre_at, a.w_pre, c0, step, D, w);
 #pragma unroll
       for (int k = 0; k < C; ++k) {
         s[0] = fmaf(x[k], x[k], s[0]);
@@ -303,7 +412,7 @@ __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const NormBwd a
     }
     // f becomes f^ (f itself without a post-norm); dh becomes G w_post
     if (post) {
-      ld_cols<kVec, C, float, kSure>(a.w_post, c0, step, D, w);
+      weight_get<kForm, kSure>(post_at, a.w_post, c0, step, D, w);
     } else {
 #pragma unroll
       for (int k = 0; k < C; ++k) w[k] = 1.f;
@@ -319,7 +428,7 @@ __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const NormBwd a
     if (kAll || a.dx) {
 #pragma unroll
       for (int k = 0; k < C; ++k) G[k] *= a.res_scale;
-      st_cols<kVec, C, float, kSure>(a.dx + t * D, c0, step, D, G);
+      store_row<kForm, kSure>(a.dx + t * D, c0, step, D, G);
     }
     if (has_f) {
       row_sums(q, red[parity][1]);
@@ -329,12 +438,12 @@ __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const NormBwd a
       const float cf = post ? -(q[0] * inv_d) : 0.f, gr = g * rf;
 #pragma unroll
       for (int k = 0; k < C; ++k) dh[k] = gr * fmaf(cf, f[k], dh[k]);
-      st_cols<kVec, C, float, kSure>(a.df + t * D, c0, step, D, dh);
+      store_row<kForm, kSure>(a.df + t * D, c0, step, D, dh);
     }
   }
   if constexpr (kStages > 0) cp_async_wait<0>();
-  if (a.part_pre) st_cols<kVec>(a.part_pre + (int64_t)blockIdx.x * ((D + 3) & ~3), c0, step, D, acc_pre);
-  if (a.part_post) st_cols<kVec>(a.part_post + (int64_t)blockIdx.x * ((D + 3) & ~3), c0, step, D, acc_post);
+  store_part<kForm>(a.part_pre, c0, step, D, acc_pre);
+  store_part<kForm>(a.part_post, c0, step, D, acc_post);
 }
 
 // dw[d] += sum over the CTAs' rows, in a fixed order: 4 columns a thread, 128
@@ -374,23 +483,43 @@ __global__ void __launch_bounds__(kReduceUnits* kReduceRows)
 // A row's threads, a multiple of 32, and columns per thread.  Vector rows: as few
 // threads as have the row in 4 units of 4 columns (the sums over the threads then
 // cost the fewest instructions per column: at 2048 columns 2 units 78.7 us
-// forward, 4 units 76.2), and as few units as these need: every unit but the last
-// is whole for all threads and needs no tests (backward of 16384 x 2048 with
-// tests 168 us, without 130).  Rows of other widths or alignment, whose loads are
-// single elements, are bound by latency: 4 columns a thread (backward of 6946 x
-// 1911 bf16 with 4 100 us, with 8 122; forward of 60000 x 301 70 and 80), the
-// forward of over 512 columns 8 with 4 CTAs on an SM (6946 x 1911 46 us, with 4
-// 62), rows of over 2048 columns 16.
+// forward, 4 units 76.2; backward 143 and 128), and as few units as these need:
+// every unit but the last is whole for all threads and needs no tests (backward of
+// 16384 x 2048 with tests 168 us, without 130).  The backward of few rows, which
+// is bound by latency, has 2 units (1237 x 1001 bf16 12.8 us, with 4 16.1; 2500 x
+// 1000 17.9 and 18.5; but 60000 x 301 90 and 67).  Rows of single elements are
+// bound by latency too: 4 columns a thread (backward of 6946 x 1911 bf16 with 4
+// 100 us, with 8 122; forward of 60000 x 301 70 and 80), the forward of over 512
+// columns 8 with 4 CTAs on an SM (6946 x 1911 46 us, with 4 62), rows of over
+// 2048 columns 16.  (The same rows by shifted units: 54 us, 39 and 29.)
 struct RowPlan {
   int threads, cols;
 };
-RowPlan row_plan(bool vec, bool forward, int64_t D) {
-  if (!vec) {
+RowPlan row_plan(Form form, bool forward, int64_t T, int64_t D) {
+  if (form == kElements) {
     const int cols = D > 4 * kMaxRowThreads ? 16 : forward && D > 512 ? 8 : 4;
     return {(int)(((D + cols - 1) / cols + 31) / 32 * 32), cols};
   }
-  const int threads = (int)((D + 511) / 512 * 32);
-  return {threads, (int)((D + 4 * threads - 1) / (4 * threads)) * 4};
+  const int64_t span = D + (form == kShifted ? 3 : 0);
+  const int64_t per_warp = !forward && T <= kFewRows && span <= 8 * kRowThreads ? 256 : 512;
+  int threads = (int)((span + per_warp - 1) / per_warp * 32), units;
+  // (where the span, but not the row, begins a unit: more threads, fewer units)
+  while ((units = (int)((span + 4 * threads - 1) / (4 * threads))), (units - 1) * 4 * threads > D) threads += 32;
+  return {threads, 4 * units};
+}
+
+// Shared memory of a vector form with kStages' rows of `row` bytes a column.
+size_t stage_bytes(Form form, int stages, const RowPlan& p, size_t row) {
+  return (size_t)p.threads * p.cols * (stages * row + (form == kShifted ? 8 : 0));
+}
+
+// The form for rows of D columns from tensors which all start on a unit or not;
+// `row`: bytes a column of a stage.  Shifted rows need room for their stages.
+Form row_form(bool units, int64_t T, int64_t D, size_t row) {
+  if (units && D % 4 == 0) return kUnits;
+  return units && D + 3 <= kMaxNormD && stage_bytes(kShifted, kStages, row_plan(kShifted, true, T, D), row) <= kMaxSmem
+             ? kShifted
+             : kElements;
 }
 
 // The backward's CTAs, each with a row of partial sums: up to 1024 threads on
@@ -411,81 +540,99 @@ cudaError_t resident_ctas(K kern, int threads, size_t smem, int n_sm, int64_t mo
   return e;
 }
 
-template <bool kVec, int C, int kStages, int kThreads, class X, class F, class H>
-cudaError_t forward_launch(const NormFwd& a, int threads, int n_sm, cudaStream_t stream) {
-  auto kern = norm_forward_kernel<kVec, C, kStages, kThreads, X, F, H>;
-  const size_t smem = (size_t)kStages * threads * C * (sizeof(X) + sizeof(F));
+// Rows of a CTA a multiple of 4 apart, unless it has one only.
+unsigned shifted_grid(unsigned grid, int64_t T) { return grid < T ? grid / 4 * 4 : grid; }
+
+template <Form kForm, int C, int kStages, int kThreads, class X, class F, class H>
+cudaError_t forward_launch(const NormFwd& a, const RowPlan& p, int n_sm, cudaStream_t stream) {
+  auto kern = norm_forward_kernel<kForm, C, kStages, kThreads, X, F, H>;
+  const size_t smem = stage_bytes(kForm, kStages, p, sizeof(X) + sizeof(F));
   unsigned grid = 0;
-  const cudaError_t e = resident_ctas(kern, threads, smem, n_sm, a.T, &grid);
+  const cudaError_t e = resident_ctas(kern, p.threads, smem, n_sm, a.T, &grid);
   if (e != cudaSuccess) return e;
-  kern<<<grid, threads, smem, stream>>>(a);
+  kern<<<kForm == kShifted ? shifted_grid(grid, a.T) : grid, p.threads, smem, stream>>>(a);
   return cudaGetLastError();
+}
+
+template <Form kForm, class X, class F, class H>
+cudaError_t forward_units(const NormFwd& a, int n_sm, cudaStream_t stream) {
+  const RowPlan p = row_plan(kForm, true, a.T, a.D);
+  if (p.threads > kRowThreads)
+    return forward_launch<kForm, 16, kStages, kMaxRowThreads, X, F, H>(a, p, n_sm, stream);
+  switch (p.cols) {
+    case 4: return forward_launch<kForm, 4, kStages, kRowThreads, X, F, H>(a, p, n_sm, stream);
+    case 8: return forward_launch<kForm, 8, kStages, kRowThreads, X, F, H>(a, p, n_sm, stream);
+    case 12: return forward_launch<kForm, 12, kStages, kRowThreads, X, F, H>(a, p, n_sm, stream);
+    default: return forward_launch<kForm, 16, kStages + 1, kRowThreads, X, F, H>(a, p, n_sm, stream);
+  }
 }
 
 template <class X, class F, class H>
-cudaError_t forward_form(const NormFwd& a, bool vec, int n_sm, cudaStream_t stream) {
-  const RowPlan p = row_plan(vec, true, a.D);
-  if (!vec)
-    return p.cols == 4   ? forward_launch<false, 4, 0, kRowThreads, X, F, H>(a, p.threads, n_sm, stream)
-           : p.cols == 8 ? forward_launch<false, 8, 0, kRowThreads, X, F, H>(a, p.threads, n_sm, stream)
-                         : forward_launch<false, 16, 0, kMaxRowThreads, X, F, H>(a, p.threads, n_sm, stream);
-  if (p.threads > kRowThreads)
-    return forward_launch<true, 16, kStages, kMaxRowThreads, X, F, H>(a, p.threads, n_sm, stream);
-  switch (p.cols) {
-    case 4: return forward_launch<true, 4, kStages, kRowThreads, X, F, H>(a, p.threads, n_sm, stream);
-    case 8: return forward_launch<true, 8, kStages, kRowThreads, X, F, H>(a, p.threads, n_sm, stream);
-    case 12: return forward_launch<true, 12, kStages, kRowThreads, X, F, H>(a, p.threads, n_sm, stream);
-    default: return forward_launch<true, 16, kStages + 1, kRowThreads, X, F, H>(a, p.threads, n_sm, stream);
-  }
+cudaError_t forward_form(const NormFwd& a, bool units, int n_sm, cudaStream_t stream) {
+  const Form form = row_form(units, a.T, a.D, sizeof(X) + sizeof(F));
+  if (form == kUnits) return forward_units<kUnits, X, F, H>(a, n_sm, stream);
+  if (form == kShifted) return forward_units<kShifted, X, F, H>(a, n_sm, stream);
+  const RowPlan p = row_plan(kElements, true, a.T, a.D);
+  return p.cols == 4   ? forward_launch<kElements, 4, 0, kRowThreads, X, F, H>(a, p, n_sm, stream)
+         : p.cols == 8 ? forward_launch<kElements, 8, 0, kRowThreads, X, F, H>(a, p, n_sm, stream)
+                       : forward_launch<kElements, 16, 0, kMaxRowThreads, X, F, H>(a, p, n_sm, stream);
 }
 
 template <class X>
-cudaError_t forward_types(const NormFwd& a, bool f_bf16, bool h_bf16, bool vec, int n_sm, cudaStream_t stream) {
+cudaError_t forward_types(const NormFwd& a, bool f_bf16, bool h_bf16, bool units, int n_sm, cudaStream_t stream) {
   if (f_bf16)
-    return h_bf16 ? forward_form<X, uint16_t, uint16_t>(a, vec, n_sm, stream)
-                  : forward_form<X, uint16_t, float>(a, vec, n_sm, stream);
-  return h_bf16 ? forward_form<X, float, uint16_t>(a, vec, n_sm, stream)
-                : forward_form<X, float, float>(a, vec, n_sm, stream);
+    return h_bf16 ? forward_form<X, uint16_t, uint16_t>(a, units, n_sm, stream)
+                  : forward_form<X, uint16_t, float>(a, units, n_sm, stream);
+  return h_bf16 ? forward_form<X, float, uint16_t>(a, units, n_sm, stream)
+                : forward_form<X, float, float>(a, units, n_sm, stream);
 }
 
-template <bool kVec, bool kAll, int C, int kStages, int kThreads, class X, class F>
-cudaError_t backward_launch(const NormBwd& a, int threads, int n_sm, int* ctas, cudaStream_t stream) {
-  auto kern = norm_backward_kernel<kVec, kAll, C, kStages, kThreads, X, F>;
-  const size_t smem = (size_t)kStages * threads * C * (8 + sizeof(X) + sizeof(F));
+template <Form kForm, bool kAll, int C, int kStages, int kThreads, class X, class F>
+cudaError_t backward_launch(const NormBwd& a, const RowPlan& p, int n_sm, int* ctas, cudaStream_t stream) {
+  auto kern = norm_backward_kernel<kForm, kAll, C, kStages, kThreads, X, F>;
+  const size_t smem = stage_bytes(kForm, kStages, p, 8 + sizeof(X) + sizeof(F));
   unsigned grid = 0;
   const cudaError_t e =
-      resident_ctas(kern, threads, smem, n_sm, std::min<int64_t>(a.T, max_backward_ctas(threads)), &grid);
+      resident_ctas(kern, p.threads, smem, n_sm, std::min<int64_t>(a.T, max_backward_ctas(p.threads)), &grid);
   if (e != cudaSuccess) return e;
+  if (kForm == kShifted) grid = shifted_grid(grid, a.T);
   *ctas = (int)grid;
-  kern<<<grid, threads, smem, stream>>>(a);
+  kern<<<grid, p.threads, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
-size_t stage_bytes(const RowPlan& p, size_t x, size_t f) { return (size_t)kStages * p.threads * p.cols * (8 + x + f); }
-
-template <bool kAll, class X, class F>
+template <Form kForm, bool kAll, class X, class F>
 cudaError_t backward_staged(const NormBwd& a, const RowPlan& p, int n_sm, int* ctas, cudaStream_t stream) {
   switch (p.cols) {
-    case 4: return backward_launch<true, kAll, 4, kStages, kRowThreads, X, F>(a, p.threads, n_sm, ctas, stream);
-    case 8: return backward_launch<true, kAll, 8, kStages, kRowThreads, X, F>(a, p.threads, n_sm, ctas, stream);
-    case 12: return backward_launch<true, kAll, 12, kStages, kRowThreads, X, F>(a, p.threads, n_sm, ctas, stream);
-    default: return backward_launch<true, kAll, 16, kStages, kRowThreads, X, F>(a, p.threads, n_sm, ctas, stream);
+    case 4: return backward_launch<kForm, kAll, 4, kStages, kRowThreads, X, F>(a, p, n_sm, ctas, stream);
+    case 8: return backward_launch<kForm, kAll, 8, kStages, kRowThreads, X, F>(a, p, n_sm, ctas, stream);
+    case 12: return backward_launch<kForm, kAll, 12, kStages, kRowThreads, X, F>(a, p, n_sm, ctas, stream);
+    default: return backward_launch<kForm, kAll, 16, kStages, kRowThreads, X, F>(a, p, n_sm, ctas, stream);
   }
 }
 
+template <Form kForm, class X, class F>
+cudaError_t backward_units(const NormBwd& a, int n_sm, int* ctas, cudaStream_t stream) {
+  const RowPlan p = row_plan(kForm, false, a.T, a.D);
+  if (p.threads > kRowThreads) {
+    if constexpr (kForm == kUnits)  // (of more than 7040 columns, two fp32 rows do not fit shared memory)
+      if (stage_bytes(kForm, kStages, p, 8 + sizeof(X) + sizeof(F)) > kMaxSmem)
+        return backward_launch<kForm, false, 16, 0, kMaxRowThreads, X, F>(a, p, n_sm, ctas, stream);
+    return backward_launch<kForm, false, 16, kStages, kMaxRowThreads, X, F>(a, p, n_sm, ctas, stream);
+  }
+  return a.dh && a.dx_out && a.f && a.w_post && a.dx && a.df
+             ? backward_staged<kForm, true, X, F>(a, p, n_sm, ctas, stream)
+             : backward_staged<kForm, false, X, F>(a, p, n_sm, ctas, stream);
+}
+
 template <class X, class F>
-cudaError_t backward_form(const NormBwd& a, bool vec, int n_sm, int* ctas, cudaStream_t stream) {
-  const RowPlan p = row_plan(vec, false, a.D);
-  if (!vec)
-    return p.cols == 4
-               ? backward_launch<false, false, 4, 0, kMaxRowThreads, X, F>(a, p.threads, n_sm, ctas, stream)
-               : backward_launch<false, false, 16, 0, kMaxRowThreads, X, F>(a, p.threads, n_sm, ctas, stream);
-  if (p.threads > kRowThreads)  // (of more than 7040 columns, two fp32 rows do not fit shared memory)
-    return stage_bytes(p, sizeof(X), sizeof(F)) <= kMaxSmem
-               ? backward_launch<true, false, 16, kStages, kMaxRowThreads, X, F>(a, p.threads, n_sm, ctas, stream)
-               : backward_launch<true, false, 16, 0, kMaxRowThreads, X, F>(a, p.threads, n_sm, ctas, stream);
-  return a.dh && a.dx_out && a.f && a.w_post && a.dx && a.df ? backward_staged<true, X, F>(a, p, n_sm, ctas, stream)
-                                                             : backward_staged<false, X, F>(a, p, n_sm, ctas, stream);
+cudaError_t backward_form(const NormBwd& a, bool units, int n_sm, int* ctas, cudaStream_t stream) {
+  const Form form = row_form(units, a.T, a.D, 8 + sizeof(X) + sizeof(F));
+  if (form == kUnits) return backward_units<kUnits, X, F>(a, n_sm, ctas, stream);
+  if (form == kShifted) return backward_units<kShifted, X, F>(a, n_sm, ctas, stream);
+  const RowPlan p = row_plan(kElements, false, a.T, a.D);
+  return p.cols == 4 ? backward_launch<kElements, false, 4, 0, kMaxRowThreads, X, F>(a, p, n_sm, ctas, stream)
+                     : backward_launch<kElements, false, 16, 0, kMaxRowThreads, X, F>(a, p, n_sm, ctas, stream);
 }
 
 bool valid(mole_dtype dt) { return dt == MOLE_F32 || dt == MOLE_BF16; }
@@ -494,7 +641,8 @@ size_t size_of(mole_dtype dt) { return dt == MOLE_BF16 ? 2 : 4; }
 // Rows of partial sums of each weight gradient, 16-byte aligned.
 int64_t part_ld(int64_t D) { return (D + 3) / 4 * 4; }
 size_t partial_bytes(int64_t T, int64_t D) {
-  const int64_t rows = std::min<int64_t>(T, max_backward_ctas(row_plan(true, false, D).threads));  // the fewest threads
+  const int most = (int)max_backward_ctas(row_plan(kUnits, true, T, D).threads);  // (with the fewest threads)
+  const int64_t rows = std::min<int64_t>(T, most);
   return ((size_t)rows * (size_t)part_ld(D) * 4 + 255) / 256 * 256;
 }
 
@@ -517,13 +665,13 @@ extern "C" mole_status mole_block_norm_forward(const void* x, mole_dtype dt_x, c
   if (st != MOLE_OK) return st;
   const int n_sm = num_sms();
   if (n_sm <= 0) return MOLE_ERR_NO_DEVICE;
-  const bool vec = D % 4 == 0 && aligned_rows(x, dt_x == MOLE_BF16) && aligned_rows(f, dt_f == MOLE_BF16) &&
+  const bool units = aligned_rows(x, dt_x == MOLE_BF16) && aligned_rows(f, dt_f == MOLE_BF16) &&
                    aligned_rows(x_out, dt_x == MOLE_BF16) && aligned_rows(h, dt_h == MOLE_BF16) &&
                    aligned16(w_post) && aligned16(w_pre);
   const NormFwd a{x, f, w_post, gate, w_pre, res_scale, eps, T, (int)D, x_out, h};
   const bool fb = dt_f == MOLE_BF16, hb = dt_h == MOLE_BF16;
-  return cuda_status(dt_x == MOLE_BF16 ? forward_types<uint16_t>(a, fb, hb, vec, n_sm, stream)
-                                       : forward_types<float>(a, fb, hb, vec, n_sm, stream));
+  return cuda_status(dt_x == MOLE_BF16 ? forward_types<uint16_t>(a, fb, hb, units, n_sm, stream)
+                                       : forward_types<float>(a, fb, hb, units, n_sm, stream));
 }
 
 extern "C" size_t mole_block_norm_backward_workspace(int64_t T, int64_t D) {
@@ -563,7 +711,7 @@ extern "C" mole_status mole_block_norm_backward(const void* x_out, mole_dtype dt
   if (st != MOLE_OK) return st;
   const int n_sm = num_sms();
   if (n_sm <= 0) return MOLE_ERR_NO_DEVICE;
-  const bool vec = D % 4 == 0 && aligned_rows(x_out, dt_x == MOLE_BF16) && aligned_rows(f, dt_f == MOLE_BF16) &&
+  const bool units = aligned_rows(x_out, dt_x == MOLE_BF16) && aligned_rows(f, dt_f == MOLE_BF16) &&
                    aligned16(w_post) && aligned16(w_pre) && aligned16(dx_out) && aligned16(dh) && aligned16(dx) &&
                    aligned16(df);
   const NormBwd a{x_out, f,  w_post, gate, w_pre, res_scale, eps,       T, (int)D,
@@ -571,11 +719,11 @@ extern "C" mole_status mole_block_norm_backward(const void* x_out, mole_dtype dt
   int ctas = 0;
   cudaError_t e;
   if (dt_x == MOLE_BF16)
-    e = dt_f == MOLE_BF16 ? backward_form<uint16_t, uint16_t>(a, vec, n_sm, &ctas, stream)
-                          : backward_form<uint16_t, float>(a, vec, n_sm, &ctas, stream);
+    e = dt_f == MOLE_BF16 ? backward_form<uint16_t, uint16_t>(a, units, n_sm, &ctas, stream)
+                          : backward_form<uint16_t, float>(a, units, n_sm, &ctas, stream);
   else
-    e = dt_f == MOLE_BF16 ? backward_form<float, uint16_t>(a, vec, n_sm, &ctas, stream)
-                          : backward_form<float, float>(a, vec, n_sm, &ctas, stream);
+    e = dt_f == MOLE_BF16 ? backward_form<float, uint16_t>(a, units, n_sm, &ctas, stream)
+                          : backward_form<float, float>(a, units, n_sm, &ctas, stream);
   if (e != cudaSuccess) return MOLE_ERR_CUDA;
   if (part_pre || part_post) {
     cudaLaunchConfig_t cfg = {};

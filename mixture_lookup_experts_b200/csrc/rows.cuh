@@ -124,10 +124,16 @@ struct RowUnit {
 };
 
 // Asynchronous copies (8 or 16 bytes) into shared memory, in groups of the
-// thread's own.
-template <int kBytes>
-__device__ __forceinline__ void cp_async(void* smem, const void* global) {
-  if constexpr (kBytes == 16)
+// thread's own.  kPart: of the first `bytes` bytes only, zeros for the rest.
+template <int kBytes, bool kPart = false>
+__device__ __forceinline__ void cp_async(void* smem, const void* global, int bytes = kBytes) {
+  if constexpr (kPart && kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem)), "l"(global), "r"(bytes)
+                 : "memory");
+  else if constexpr (kPart)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(smem)), "l"(global), "r"(bytes)
+                 : "memory");
+  else if constexpr (kBytes == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(global) : "memory");
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(smem)), "l"(global) : "memory");

@@ -182,6 +182,57 @@ def test_unaligned_rows(mole):
     assert float(buf[0]) == 3.0 and float(buf[-1]) == 3.0
 
 
+# Rows that start anywhere in a unit of 4: every width mod 4, widths around a
+# thread's or a unit's end, more rows than CTAs (each shift takes its own ones),
+# and widths whose rows are too long for the shifted units.
+@pytest.mark.parametrize("T,D", [(6, 125), (9, 126), (7, 127), (4, 383), (5, 767), (3, 1534), (4, 1535), (3, 2046),
+                                 (4, 2047), (5, 4093), (3, 4095), (2, 5633), (2, 7041), (2, 8189), (2, 8190), (3, 8191),
+                                 (4001, 61), (3000, 130), (2600, 131), (1700, 641), (1501, 1153)])
+@pytest.mark.parametrize("tx,tf", [(F32, BF16), (BF16, F32)])
+def test_shifted_rows(mole, T, D, tx, tf):
+    rng = np.random.default_rng(D)
+    x, f, w_post, g, w_pre = _layer(rng, T + 1, D, tx, tf)
+    x[T], f[T], g[T] = float("nan"), float("nan"), float("nan")  # behind the batch: must not get in
+    x, f, g = x[:T], f[:T], g[:T]
+    dx_out, dh = _rand(rng, T, D), _rand(rng, T, D)
+    _check_backward(mole, x, f, w_post, g, 0.7, w_pre, dx_out, dh)
+    _check_backward(mole, x, f, w_post, None, 0.7, w_pre, None, dh)
+    _check_forward(mole, x, f, w_post, g, 0.8, w_pre, BF16)
+    _check_forward(mole, x, f, w_post, g, 0.8, w_pre, F32, in_place=True)
+
+
+def test_shifted_rows_alone(mole):
+    # a unit that two rows share: NaN in one stays there, and nothing is written behind the last row
+    rng = np.random.default_rng(13)
+    T, D = 2500, 67
+    x, f, w_post, g, w_pre = _layer(rng, T, D, F32, F32)
+    dx_out, dh = _rand(rng, T, D), _rand(rng, T, D)
+    bad = torch.arange(1, T, 2, device="cuda")
+    good = torch.arange(0, T, 2, device="cuda")
+    want = (*mole.mole_block_norm_forward(x, f, w_post, g, 0.8, w_pre, EPS, h_dtype=F32),
+            *mole.mole_block_norm_backward(x, dx_out, dh, f, w_post, g, 0.8, w_pre, EPS))
+    for t in (x, f, dx_out, dh):
+        t[bad] = float("nan")
+    bufs = [torch.full((T + 1, D), 5.0, device="cuda") for _ in range(4)]
+    mole.mole_block_norm_forward(x, f, w_post, g, 0.8, w_pre, EPS, x_out=bufs[0][:T], h=bufs[1][:T])
+    _, _, dgate = mole.mole_block_norm_backward(x, dx_out, dh, f, w_post, g, 0.8, w_pre, EPS, dx=bufs[2][:T],
+                                                df=bufs[3][:T])
+    assert mole.mole_check() == 0
+    for got, w in zip((*bufs, dgate), want):
+        assert torch.equal(got[good], w[good])
+    assert all(bool((b[T] == 5.0).all()) for b in bufs)
+
+
+@pytest.mark.parametrize("T,D", [(30, 301), (20, 1001), (5, 3001)])
+def test_element_rows(mole, T, D):
+    # tensors that start inside a unit, rows of every kind of width
+    rng = np.random.default_rng(14)
+    _, f, w_post, g, w_pre = _layer(rng, T, D, BF16, F32)
+    x = _rand(rng, T * D + 1, dtype=BF16)[1:].view(T, D)
+    _check_forward(mole, x, f, w_post, g, 0.8, w_pre, BF16)
+    _check_backward(mole, x, f, w_post, g, 0.8, w_pre, _rand(rng, T, D), _rand(rng, T, D))
+
+
 def test_graph_and_stream(mole):
     rng = np.random.default_rng(12)
     T, D = 500, 256
