@@ -162,6 +162,20 @@ def test_backward_from_unaligned_rows(mole):
     assert float(buf[0]) == 0.0 and float(buf[-1]) == 0.0
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("offset", [0, 1, 2, 3])
+@pytest.mark.parametrize("T,V,D", [(1501, 90, 1), (1100, 400, 3), (2049, 37, 67), (1027, 9, 131), (1301, 700, 1613),
+                                   (1025, 2000, 514), (4097, 60, 34)])
+def test_backward_single_columns(mole, T, V, D, offset, dtype):
+    # rows that are no vector ones, from every place of a tensor in 4 elements: all
+    # columns, the first and the last of the tensor among them, and no other's
+    rng = np.random.default_rng(D)
+    buf = torch.full((offset + T * D + 1,), float("nan"), dtype=dtype, device="cuda")
+    dout = buf[offset:offset + T * D].view(T, D)
+    dout.copy_(_rand(rng, T, D, dtype=dtype))
+    _check_backward(mole, rng, T, V, D, dtype, rng.integers(0, V, T).astype(np.int32), dout=dout)
+
+
 def test_backward_large_batch_and_vocabulary(mole):
     # 200000 tokens over 2^24 + ids (four digits of key), checked by torch in fp64
     rng = np.random.default_rng(7)
