@@ -80,6 +80,81 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_forward_kernel(const int3
   }
 }
 
+// Rows of a bf16 table that start inside a unit of 4 columns (D no multiple of
+// 4), table and output starting on one: the units are those of out, shifted by up
+// to 3 columns, so that stores are whole but at a row's ends; a unit's columns
+// come from the two units of E that they lie in (the second one is the next
+// thread's first: one read of memory), joined by the row's distance.  Half the
+// accesses of single columns: 16384 x 2049 to bf16 38 us, by those 47; to fp32 47
+// and 55.  (With an fp32 table the second unit costs more than it saves: 72 and 52.)
+
+// The unit at element i (a multiple of 4) of E's n elements; what lies outside
+// is not read.
+__device__ __forceinline__ uint2 load_inside(const uint16_t* E, int64_t i, int64_t n) {
+  if (i >= 0 && i + 4 <= n) return *reinterpret_cast<const uint2*>(E + i);
+  uint32_t x[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x[k] = i + k >= 0 && i + k < n ? E[i + k] : 0;
+  return make_uint2(x[0] | (x[1] << 16), x[2] | (x[3] << 16));
+}
+
+// Columns d .. d + 3 of two units.
+__device__ __forceinline__ void join_units(uint2 x, uint2 next, int d, float (&f)[4]) {
+  const uint32_t a[3] = {d & 2 ? x.y : x.x, d & 2 ? next.x : x.y, d & 2 ? next.y : next.x};
+  const uint32_t lo = d & 1 ? __funnelshift_r(a[0], a[1], 16) : a[0];
+  const uint32_t hi = d & 1 ? __funnelshift_r(a[1], a[2], 16) : a[1];
+  f[0] = bf16_lo(lo); f[1] = bf16_hi(lo); f[2] = bf16_lo(hi); f[3] = bf16_hi(hi);
+}
+
+template <class Out, int kRows>
+__global__ void __launch_bounds__(kEmbedThreads)
+    embed_forward_shifted_kernel(const int32_t* __restrict__ ids, int64_t T, const uint16_t* __restrict__ E, int64_t V,
+                                 int D, float scale, Out* __restrict__ out, unsigned* err) {
+  const int tx = blockDim.x;
+  const int unit0 = blockIdx.y * tx * 8 + 4 * (int)threadIdx.x;  // the first unit's place; the second: 4 tx on
+  const int64_t t0 = ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * kRows, n = V * D;
+  int32_t id[kRows];
+  uint2 x[kRows][2], next[kRows][2];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) id[r] = t0 + r < T ? __ldg(ids + t0 + r) : -1;
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    if (id[r] < 0 || (int64_t)id[r] >= V) continue;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int col = unit0 + 4 * u * tx - (int)(((t0 + r) * D) & 3);
+      if (col >= D) continue;
+      const int64_t first = (int64_t)id[r] * D + col;
+      x[r][u] = load_inside(E, first & ~(int64_t)3, n);
+      if (first & 3) next[r][u] = load_inside(E, (first & ~(int64_t)3) + 4, n);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    if (t0 + r >= T) return;
+    const bool ok = id[r] >= 0 && (int64_t)id[r] < V;
+    if (!ok && threadIdx.x == 0 && blockIdx.y == 0) atomicOr(err, kErrIndex);
+    const int shift = (int)(((t0 + r) * D) & 3), d = (int)(((int64_t)id[r] * D - shift) & 3);
+    Out* row = out + (t0 + r) * D;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int col = unit0 + 4 * u * tx - shift;
+      if (col >= D) continue;
+      float f[4];
+      join_units(x[r][u], next[r][u], d, f);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[k] = ok ? f[k] * scale : NAN;
+      if (col >= 0 && col + 4 <= D) {
+        st_unit(row + col, f[0], f[1], f[2], f[3]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (col + k >= 0 && col + k < D) st1(row + col + k, f[k]);
+      }
+    }
+  }
+}
+
 // ---- gradient, step 1: the stable sort ----
 struct SortArgs {
   const int32_t* ids;
@@ -780,23 +855,26 @@ cudaError_t launch_small(const int32_t* ids, int64_t T, int64_t V, int passes, c
   return cudaGetLastError();
 }
 
-// Rows per thread: 4 once that leaves a CTA for every SM.
-template <bool kVec, class In, class Out>
-void launch_forward(const int32_t* ids, int64_t T, const void* E, int64_t V, int D, float scale, void* out,
-                    unsigned* err, int n_sm, cudaStream_t stream) {
-  const RowSplit s = row_split(D, 8, kEmbedThreads);
+// Rows per thread: 4 (2 of the shifted form, whose rows take twice the registers)
+// once that leaves a CTA for every SM.
+template <class In, class Out>
+void launch_forward(const int32_t* ids, int64_t T, const In* E, int64_t V, int D, float scale, Out* out, unsigned* err,
+                    int n_sm, cudaStream_t stream) {
+  constexpr bool kBf16 = sizeof(In) == 2;
+  const bool units = aligned_rows(E, kBf16) && aligned_rows(out, sizeof(Out) == 2), vec = units && D % 4 == 0;
+  const bool shifted = units && !vec && kBf16;
+  const RowSplit s = row_split(D + (shifted ? 3 : 0), 8, kEmbedThreads);
   const dim3 block(s.tx, kEmbedThreads / s.tx);
   const bool many = T * s.slices >= (int64_t)n_sm * 4 * block.y;
-  const dim3 grid((unsigned)((T + block.y * (many ? 4 : 1) - 1) / (block.y * (many ? 4 : 1))), s.slices);
-  (many ? embed_forward_kernel<kVec, In, Out, 4> : embed_forward_kernel<kVec, In, Out, 1>)<<<grid, block, 0, stream>>>(
-      ids, T, static_cast<const In*>(E), V, D, scale, static_cast<Out*>(out), err);
-}
-
-template <class In, class Out>
-void forward_rows(bool vec, const int32_t* ids, int64_t T, const void* E, int64_t V, int D, float scale, void* out,
-                  unsigned* err, int n_sm, cudaStream_t stream) {
-  (vec ? launch_forward<true, In, Out> : launch_forward<false, In, Out>)(ids, T, E, V, D, scale, out, err, n_sm,
-                                                                        stream);
+  const unsigned rows = block.y * (many ? shifted ? 2 : 4 : 1);
+  const dim3 grid((unsigned)((T + rows - 1) / rows), s.slices);
+  auto kern = vec    ? many ? embed_forward_kernel<true, In, Out, 4> : embed_forward_kernel<true, In, Out, 1>
+              : many ? embed_forward_kernel<false, In, Out, 4>
+                     : embed_forward_kernel<false, In, Out, 1>;
+  if constexpr (kBf16) {
+    if (shifted) kern = many ? embed_forward_shifted_kernel<Out, 2> : embed_forward_shifted_kernel<Out, 1>;
+  }
+  kern<<<grid, block, 0, stream>>>(ids, T, E, V, D, scale, out, err);
 }
 
 }  // namespace
@@ -806,13 +884,9 @@ mole_status embed_forward(const int32_t* ids, int64_t T, const void* E, int64_t 
   unsigned* err = error_word();
   const int n_sm = num_sms();
   if (!err || n_sm <= 0) return MOLE_ERR_CUDA;
-  const bool vec = D % 4 == 0 && aligned_rows(E, E_bf16) && aligned_rows(out, out_bf16);
-  if (E_bf16)
-    (out_bf16 ? forward_rows<uint16_t, uint16_t> : forward_rows<uint16_t, float>)(vec, ids, T, E, V, (int)D, scale, out,
-                                                                                 err, n_sm, stream);
-  else
-    (out_bf16 ? forward_rows<float, uint16_t> : forward_rows<float, float>)(vec, ids, T, E, V, (int)D, scale, out, err,
-                                                                           n_sm, stream);
+  auto rows = [&](auto* e, auto* o) { launch_forward(ids, T, e, V, (int)D, scale, o, err, n_sm, stream); };
+  auto types = [&](auto* e) { out_bf16 ? rows(e, static_cast<uint16_t*>(out)) : rows(e, static_cast<float*>(out)); };
+  E_bf16 ? types(static_cast<const uint16_t*>(E)) : types(static_cast<const float*>(E));
   return cuda_status(cudaGetLastError());
 }
 

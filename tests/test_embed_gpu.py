@@ -63,6 +63,28 @@ def test_forward_from_unaligned_rows(mole):
     assert torch.equal(out, (E[dev(ids).long()] * 2.0).to(BF16)) and float(out_buf[0]) == 7.0
 
 
+# Widths that are no multiple of 4: rows of the table and of the output start at
+# different places in a unit; one row a thread and four; a table that ends
+# inside a unit, its last row and its first one among the ids.
+@pytest.mark.parametrize("tin", [F32, BF16])
+@pytest.mark.parametrize("tout", [F32, BF16])
+@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("T,V,D", [(50, 5, 1), (40, 7, 2), (61, 3, 5), (10001, 51, 67), (12000, 31, 130), (6001, 7, 301),
+                                   (700, 9, 2045), (300, 5, 2046), (211, 3, 2047)])
+def test_forward_shifted_rows(mole, T, V, D, offset, tin, tout):
+    rng = np.random.default_rng(D)
+    buf = _rand(rng, offset + V * D, dtype=tin)  # (offset 1: single columns)
+    E = buf[offset:].view(V, D)
+    ids = rng.integers(0, V, T).astype(np.int32)
+    ids[0], ids[-1], ids[T // 2] = 0, V - 1, -3
+    out = torch.full((T + 1, D), 7.0, dtype=tout, device="cuda")
+    mole.mole_embed_forward(dev(ids), E, 2.0, out=out[:T])
+    assert mole.mole_check() == 5
+    keep = torch.from_numpy(ids >= 0).cuda()
+    assert torch.equal(out[:T][keep], (E[dev(ids).long()[keep]] * 2.0).to(tout))
+    assert torch.isnan(out[T // 2]).all() and bool((out[T] == 7.0).all())
+
+
 def test_forward_table_beyond_2_31_elements(mole):
     # row offsets pass 32 bits: 2^31 + elements of bf16
     V, D = 1048600, 2056
