@@ -85,8 +85,8 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_forward_kernel(const int3
 // to 3 columns, so that stores are whole but at a row's ends; a unit's columns
 // come from the two units of E that they lie in (the second one is the next
 // thread's first: one read of memory), joined by the row's distance.  Half the
-// accesses of single columns: 16384 x 2049 to bf16 38 us, by those 47; to fp32 47
-// and 55.  (With an fp32 table the second unit costs more than it saves: 72 and 52.)
+// accesses of single columns: 16384 x 2049 to bf16 38 us, by those 55; to fp32 47
+// and 61.  (With an fp32 table the second unit costs more than it saves: 72 and 52.)
 
 // The unit at element i (a multiple of 4) of E's n elements; what lies outside
 // is not read.

@@ -78,11 +78,13 @@ __device__ __forceinline__ void st_cols(T* row, int col0, int step, int D, const
   }
 }
 
-// A thread's C columns of a row as loaded (converted when they are used, so
-// that a load in flight holds no more registers than its bytes).
+// A thread's C columns of a row as loaded: converted when they are used, so that
+// a load in flight holds no more registers than its bytes; single bf16 columns
+// have a register each (packing two of them waits for both: the gradient of 16384
+// x 1001 bf16 61.5 us, so 46.8).
 template <bool kVec, class T, int C>
 struct RowUnit {
-  static constexpr int kWords = (C * (int)sizeof(T) + 3) / 4;
+  static constexpr int kWords = kVec ? C * (int)sizeof(T) / 4 : C;
   uint32_t w[kWords];
   __device__ __forceinline__ void load(const T* row, int col0, int step, int D) {
     if constexpr (kVec) {
@@ -98,18 +100,14 @@ struct RowUnit {
         }
       }
     } else {
-      uint32_t x[C];
 #pragma unroll
       for (int k = 0; k < C; ++k) {
         const int c = col0 + k * step;
         if constexpr (sizeof(T) == 4)
-          x[k] = c < D ? __float_as_uint(row[c]) : 0u;
+          w[k] = c < D ? __float_as_uint(row[c]) : 0u;
         else
-          x[k] = c < D ? (uint32_t)row[c] : 0u;
+          w[k] = c < D ? (uint32_t)row[c] : 0u;
       }
-#pragma unroll
-      for (int i = 0; i < kWords; ++i)
-        w[i] = sizeof(T) == 4 ? x[i] : 2 * i + 1 < C ? x[2 * i] | (x[(2 * i + 1) % C] << 16) : x[2 * i];
     }
   }
   __device__ __forceinline__ void get(float (&f)[C]) const {
@@ -118,7 +116,7 @@ struct RowUnit {
       if constexpr (sizeof(T) == 4)
         f[k] = __uint_as_float(w[k]);
       else
-        f[k] = k & 1 ? bf16_hi(w[k / 2]) : bf16_lo(w[k / 2]);
+        f[k] = !kVec ? bf16_lo(w[k]) : k & 1 ? bf16_hi(w[k / 2]) : bf16_lo(w[k / 2]);
     }
   }
 };
