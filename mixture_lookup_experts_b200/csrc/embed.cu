@@ -524,9 +524,9 @@ __device__ __forceinline__ void leave_run(const SumArgs& a, int64_t c, int id) {
 // has kUnits units of 4 columns, 4 * blockDim.x apart: accesses to dout and to
 // dE are both contiguous over a warp, and the bookkeeping of a token serves all
 // of them.  (Loads into registers, 8 tokens at a time: 47 us for 16384 Zipf
-// tokens of 2048 fp32, this form 36; 1, 2 and 4 units and 4 to 14 slots: 2 and 5
+// tokens of 2048 fp32, this form 34; 1, 2 and 4 units and 4 to 14 slots: 2 and 5
 // are the fastest together.)  Bound by HBM for ids that hardly repeat (65536 x
-// 1024 bf16: 70 us against 66 at the copy rate), for text by the last CTAs: 9 us
+// 1024 bf16: 67 us against 66 at the copy rate), for text by the last CTAs: 9 us
 // each, which nothing overlaps at the end.
 template <class In, int kUnits, int kSlots>
 __global__ void __launch_bounds__(kChunkThreads) embed_chunk_kernel(const SumArgs a) {

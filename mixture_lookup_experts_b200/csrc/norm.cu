@@ -6,8 +6,8 @@
 // A token's row is held in registers, up to 16 columns a thread, by a CTA of one
 // to 16 warps; the row's sums are reduced by shuffles and (beyond one warp)
 // shared memory.  Each tensor is read and written once: both kernels are bound
-// by HBM (16384 x 2048 fp32: forward 74 us, backward 131 us and 6 us for the
-// weight gradients' join; 71.7 and 123 us at the copy rate).
+// by HBM (16384 x 2048 fp32: forward 73 to 76 us, backward 127 to 129 us and 6 us
+// for the weight gradients' join; 71.7 and 123 us at the copy rate).
 //
 // Backward, per token (n = D, r = 1/rms):
 //     G  = dx' + r_x (a - x^ <a, x^>/n)      a = dh w_pre,  x^ = x' r_x
