@@ -201,6 +201,22 @@ def test_shifted_rows(mole, T, D, tx, tf):
     _check_forward(mole, x, f, w_post, g, 0.8, w_pre, F32, in_place=True)
 
 
+@pytest.mark.parametrize("post", [False, True])
+@pytest.mark.parametrize("gate", [False, True])
+def test_shifted_rows_parts(mole, post, gate):
+    rng = np.random.default_rng(15)
+    T, D = 2700, 323
+    x, f, w_post, g, w_pre = _layer(rng, T, D, F32, BF16, post, gate)
+    dx_out, dh = _rand(rng, T, D), _rand(rng, T, D)
+    _check_forward(mole, x.clone(), f, w_post, g, 1.0, None, BF16)
+    _check_forward(mole, x.clone(), f, w_post, g, -0.5, w_pre, BF16, in_place=True)
+    _check_forward(mole, x, None, None, None, 1.0, w_pre, F32)
+    _check_backward(mole, x, f, w_post, g, 0.6, None, dx_out, None)
+    _check_backward(mole, x, f, w_post, g, 0.6, w_pre, None, dh)
+    _check_backward(mole, x, f, w_post, g, 0.6, w_pre, dx_out.clone(), dh.clone(), alias=True)
+    _check_backward(mole, x, None, None, None, 0.6, w_pre, dx_out, dh)
+
+
 def test_shifted_rows_alone(mole):
     # a unit that two rows share: NaN in one stays there, and nothing is written behind the last row
     rng = np.random.default_rng(13)
