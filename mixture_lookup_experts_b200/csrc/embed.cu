@@ -39,7 +39,7 @@ constexpr int kChunkThreads = 128;
 constexpr int kJoinThreads = 256;
 constexpr int kChunkUnits = 2, kChunkSlots = 5, kScalarCols = 4;
 constexpr int64_t kChunkGroups = 1776;  // chunks times slices: 12 CTAs for each of 148 SMs
-constexpr int kSmallTokens = 1024;
+constexpr int kSmallTokens = 1024, kSmallBatch = 8;
 constexpr int kOneCtaTokens = 2048;
 
 // ---- forward ----
@@ -708,30 +708,30 @@ __global__ void __launch_bounds__(kJoinThreads, 4) embed_join_kernel(const SumAr
 }
 
 // ---- gradient of a small batch (T <= kSmallTokens): one launch ----
-// CTA = a strip of 32 columns, one a lane (any width and alignment).  Every CTA
+// CTA = a strip of G columns, one a lane (any width and alignment).  Every CTA
 // sorts the whole batch in its shared memory (a few us; the other strips do the
-// same beside it), its 32 warps sum equal shares of the sorted tokens, and the
-// runs that cross a share are joined from shared memory.
-template <class In>
+// same beside it), its kSortThreads / G groups of G lanes sum equal shares of the
+// sorted tokens, and the runs that cross a share are joined from shared memory.
+template <class In, int G>
 __global__ void __launch_bounds__(kSortThreads, 1)
     embed_small_kernel(const int32_t* __restrict__ ids, int T, int64_t V, int passes, const In* __restrict__ dout,
                        int D, float scale, float* dE, unsigned* err) {
-  constexpr int kQ = 8;
+  constexpr int kShares = kSortThreads / G;
   extern __shared__ __align__(16) uint8_t sort_smem[];
   SortSmem& s = *reinterpret_cast<SortSmem*>(sort_smem);
   int2* sorted = reinterpret_cast<int2*>(sort_smem + sizeof(SortSmem));  // [kSmallTokens]
-  float* part = reinterpret_cast<float*>(sorted + kSmallTokens);         // [kSortWarps][2][32]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float* part = reinterpret_cast<float*>(sorted + kSmallTokens);         // [kShares][2][G]
+  const int lane = threadIdx.x % G, group = threadIdx.x / G;
   cta_sort<kSmallTokens / kSortThreads>(s, ids, T, V, passes, sorted, err);
-  const int col = blockIdx.x * 32 + lane;
-  auto begin = [&](int w) { return (int)((int64_t)T * w / kSortWarps); };
-  const int p0 = begin(warp), p1 = begin(warp + 1);
-  float* entering = part + warp * 64 + lane;
-  float* leaving = entering + 32;
+  const int col = blockIdx.x * G + lane;
+  auto begin = [&](int w) { return (int)((int64_t)T * w / kShares); };
+  const int p0 = begin(group), p1 = begin(group + 1);
+  float* entering = part + group * 2 * G + lane;
+  float* leaving = entering + G;
   int owner = -1;  // the id of the run that begins in this share and leaves it
   if (p0 < p1 && col < D)
-    sum_runs<In, 1, kQ>(
-        dout, dE, D, scale, (int)V, p0, p1, T, p0 > 0 ? sorted[p0 - 1].x : -1, col, 32,
+    sum_runs<In, 1, kSmallBatch>(
+        dout, dE, D, scale, (int)V, p0, p1, T, p0 > 0 ? sorted[p0 - 1].x : -1, col, G,
         [&](int p) { return sorted[p]; }, [&](const float(&acc)[1]) { *entering = acc[0]; },
         [&](int id, const float(&acc)[1]) {
           owner = id;
@@ -742,11 +742,11 @@ __global__ void __launch_bounds__(kSortThreads, 1)
   float* to = dE + (int64_t)owner * D + col;
   const float before = *to;
   float acc = *leaving;
-  for (int w = warp + 1; w < kSortWarps; ++w) {
+  for (int w = group + 1; w < kShares; ++w) {
     const int q0 = begin(w);
     if (q0 == begin(w + 1)) continue;  // an empty share
     if (sorted[q0].x != owner) break;
-    acc += part[w * 64 + lane];
+    acc += part[w * 2 * G + lane];
   }
   *to = fmaf(scale, acc, before);
 }
@@ -844,14 +844,20 @@ cudaError_t launch_sort_one(const SortArgs& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+// Strips of 16 columns where shares of 32-column strips take more than a batch of
+// tokens and an SM has one strip at most: the shares are half as long then (777
+// tokens of 1001 bf16 10.3 us, by 32 columns 12.3; 1024 of 1000 10.9 and 14.4;
+// but 40 of 1272 7.5 and 6.8).  Strips of 8 gain no more (10.3).
 template <class In>
 cudaError_t launch_small(const int32_t* ids, int64_t T, int64_t V, int passes, const void* dout, int D, float scale,
-                         float* dE, unsigned* err, cudaStream_t stream) {
-  const int smem = (int)sizeof(SortSmem) + kSmallTokens * 8 + kSortWarps * 64 * 4;
-  const cudaError_t e = allow_smem(embed_small_kernel<In>);
+                         float* dE, unsigned* err, int n_sm, cudaStream_t stream) {
+  const int smem = (int)sizeof(SortSmem) + kSmallTokens * 8 + kSortThreads * 2 * 4;
+  const int G = T > kSmallBatch * 32 && D <= 16 * n_sm ? 16 : 32;
+  auto kern = G == 16 ? embed_small_kernel<In, 16> : embed_small_kernel<In, 32>;
+  const cudaError_t e = allow_smem(kern);
   if (e != cudaSuccess) return e;
-  embed_small_kernel<In><<<(unsigned)((D + 31) / 32), kSortThreads, smem, stream>>>(
-      ids, (int)T, V, passes, static_cast<const In*>(dout), D, scale, dE, err);
+  kern<<<(unsigned)((D + G - 1) / G), kSortThreads, smem, stream>>>(ids, (int)T, V, passes,
+                                                                    static_cast<const In*>(dout), D, scale, dE, err);
   return cudaGetLastError();
 }
 
@@ -907,7 +913,7 @@ mole_status embed_backward(const int32_t* ids, int64_t T, const void* dout, bool
   cudaError_t e;
   if (T <= kSmallTokens)
     return cuda_status((bf16 ? launch_small<uint16_t> : launch_small<float>)(ids, T, V, passes, dout, (int)D, scale, dE,
-                                                                            err, stream));
+                                                                            err, n_sm, stream));
   const SortArgs sa{ids, T, V, w.buf[0], w.buf[1], passes, w.n_runs, err};
   if (T <= kOneCtaTokens)
     e = launch_sort_one(sa, stream);

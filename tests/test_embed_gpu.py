@@ -143,6 +143,15 @@ def test_backward_runs_that_end_on_chunk_borders(mole):
     _check_backward(mole, rng, ids.size, 21, 64, BF16, rng.permutation(ids))
 
 
+@pytest.mark.parametrize("T,V,D", [(256, 30, 33), (257, 30, 33), (258, 2, 17), (511, 60, 100), (777, 4, 2368),
+                                   (1024, 900, 2369), (1023, 1, 15), (300, 200, 16)])
+def test_backward_small_batches(mole, T, V, D):
+    # one launch: shares of every length, runs across many shares, strips of both widths
+    rng = np.random.default_rng(T)
+    _check_backward(mole, rng, T, V, D, BF16, rng.integers(0, V, T).astype(np.int32))
+    _check_backward(mole, rng, T, V, D, F32, np.sort(rng.integers(-1, V, T)).astype(np.int32))
+
+
 def test_backward_bad_ids(mole):
     rng = np.random.default_rng(4)
     T, V, D = 777, 60, 96
