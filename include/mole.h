@@ -457,6 +457,8 @@ mole_status mole_block_norm_backward(const void* x_out, mole_dtype dt_x, const v
  * there is one, else param), and t the step number, counted from 1:
  *     m = beta1 m + (1 - beta1) g        v = beta2 v + (1 - beta2) g^2
  *     p = p - lr weight_decay p - lr m / (1 - beta1^t) / (sqrt(v / (1 - beta2^t)) + eps)
+ * eps is 0 to 2^125, and one below 2^-126 counts as 2^-126: an element whose m
+ * is zero takes a step of zero, also where v and eps are zero.
  * param = p rounded to its type (and master = p).  A bf16 param without a
  * master rounds to nearest every step, so updates below half a bf16 step of
  * the weight are lost; with a master they add up.

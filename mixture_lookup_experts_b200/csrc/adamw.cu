@@ -35,6 +35,7 @@ constexpr int kAdamTensors = 128;                          // per launch (10 KB 
 constexpr float kInvE4m3Max = (float)(1.0 / 448.0);
 constexpr float kScaleFloor = 0x1p-120f;                   // its reciprocal is finite
 constexpr float kE4m3Tiny = 0x1p-9f;                       // the smallest nonzero code
+constexpr float kEpsMin = 0x1p-126f, kEpsMax = 0x1p125f;   // well inside what fast_rcp has
 
 struct AdamTensor {
   void* param;
@@ -135,7 +136,8 @@ __device__ __forceinline__ uint32_t encode(const float (&f)[4]) {
   return lo | (hi << 16);
 }
 
-// 1 / x for x that is zero, infinite, NaN or in [2^-126, 2^126] (1 ulp).
+// 1 / x for x that is infinite, NaN or in [2^-126, 2^126] (1 ulp); subnormal x
+// count as zero.
 __device__ __forceinline__ float fast_rcp(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -216,7 +218,9 @@ __device__ __forceinline__ void step_chunk(const AdamArgs& a, const AdamTensor& 
       m[u][k] = __fadd_rn(__fmul_rn(m[u][k], a.b1), __fmul_rn(g[u][k], a.omb1));
       v[u][k] = __fadd_rn(__fmul_rn(v[u][k], a.b2), __fmul_rn(__fmul_rn(g[u][k], g[u][k]), a.omb2));
       r[u][k] = __fsqrt_rn(v[u][k]);
-      // (the root of a v that is not zero is at least 2^-75: no subnormal here)
+      // (eps is in [2^-126, 2^125], and the root, up to 2^64, and its factor, up to
+      // 2^27, add to it: the reciprocal is finite and not zero but for a v that is
+      // not finite, and an m of zero makes a step of zero whatever v and eps)
       const float step = m[u][k] * fast_rcp(fmaf(r[u][k], w.root, a.eps));
       p[u][k] = fmaf(-w.step_size, step, fmaf(-decay, p[u][k], p[u][k]));
       if constexpr (kState8) {
@@ -329,7 +333,8 @@ bool overlapping(std::vector<Range>& r) {
 
 mole_status check_adamw(const mole_adamw_tensor* tensors, int32_t n_tensors, const mole_adamw_config* c) {
   if (n_tensors < 0 || !c || (n_tensors > 0 && !tensors)) return MOLE_ERR_ARG;
-  if (!(c->beta1 >= 0.0 && c->beta1 < 1.0) || !(c->beta2 >= 0.0 && c->beta2 < 1.0) || !(c->eps >= 0.0))
+  if (!(c->beta1 >= 0.0 && c->beta1 < 1.0) || !(c->beta2 >= 0.0 && c->beta2 < 1.0) ||
+      !(c->eps >= 0.0 && c->eps <= (double)kEpsMax))
     return MOLE_ERR_ARG;
   if (!c->step_dev && c->step < 1) return MOLE_ERR_ARG;
   if (c->state8 != 0 && c->state8 != 1) return MOLE_ERR_ARG;
@@ -375,7 +380,7 @@ mole_status run_adamw(const mole_adamw_tensor* tensors, int32_t n_tensors, const
   a.omb1 = (float)(1.0 - c->beta1);
   a.b2 = (float)c->beta2;
   a.omb2 = (float)(1.0 - c->beta2);
-  a.eps = (float)c->eps;
+  a.eps = std::max((float)c->eps, kEpsMin);
   a.beta1 = c->beta1;
   a.beta2 = c->beta2;
   a.lr_host = c->lr;

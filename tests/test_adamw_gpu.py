@@ -248,3 +248,31 @@ def test_large_tensor(mole):
     for x, want in ((p, -0.1), (m, 1e-4), (v, 1e-8)):
         lo, hi = float(x.min()), float(x.max())
         assert abs(lo - want) <= 32 * ref.U * abs(want) and abs(hi - want) <= 32 * ref.U * abs(want)
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-50, 1e-40, 2.0 ** -126, 1e-30])
+@pytest.mark.parametrize("param", ["f32", "master", "bf16"])
+@pytest.mark.parametrize("state", [32, 8])
+def test_zero_moments_with_an_eps_near_zero(mole, param, state, eps):
+    # zero states and, for every other run of elements, no gradient (the rows of
+    # an embedding that a batch does not hold): nothing but the decay moves them
+    rng = np.random.default_rng(10)
+    n = 5003
+    t = _tensor(rng, n, param, F32, state)
+    for k in ("m", "v", "sm", "sv"):
+        if t[k] is not None:
+            t[k].view(torch.uint8).zero_()
+    still = np.arange(n) // 50 % 2 == 0
+    t["g"][torch.from_numpy(still).cuda()] = 0.0
+    t["g"][torch.from_numpy(~still).cuda()] += 1e-6
+    host = {k: None if x is None else x.clone() for k, x in t.items()}
+    _step(mole, [t], 0.1, eps=eps, step=1)
+    assert mole.mole_check() == 0
+    with np.errstate(divide="ignore", invalid="ignore"):
+        want = [np.array(x) for x in _expect(host, 0.1, eps=eps, step=1)]
+    p0 = ref.f64(host["w"] if host["w"] is not None else host["p"])
+    # the decay of a weight whose step is zero: three roundings
+    decayed = p0 - HYPER["lr"] * float(np.float32(0.1)) * p0
+    want[0] = np.where(still, decayed, want[0])
+    want[3] = np.where(still, 4 * ref.U * np.abs(p0), want[3])
+    _check(t, want)

@@ -242,3 +242,10 @@ def test_adamw_form_against_torch():
         opt.step()
         q, m, v = ref.adamw(q, g, m, v, 1e-2, 0.9, 0.95, 1e-6, step, 0.1)[:3]
         np.testing.assert_allclose(q, p.detach().numpy(), rtol=1e-12)
+
+
+def test_adamw_eps_range(mole):
+    for eps, status in ((0.0, NO_DEVICE), (1e-50, NO_DEVICE), (2.0 ** 125, NO_DEVICE), (2.0 ** 125 * 1.001, 1),
+                        (1e300, 1), (float("inf"), 1)):
+        t, cfg = _adam(mole, 1, eps=eps)
+        assert mole.lib.mole_adamw_step(t, 1, ctypes.addressof(cfg), None) == status, eps
