@@ -271,3 +271,49 @@ def test_empty_batch(mole):
     dE = torch.ones(4, 8, device="cuda")
     mole.mole_embed_backward(ids, torch.empty(0, 8, device="cuda"), dE)
     assert mole.mole_check() == 0 and bool((dE == 1).all())
+
+
+def _check_between_rows(mole, ids, dout, V, scale=1.3):
+    """The gradient into rows 1 .. V of a buffer, by torch in fp64: what the
+    batch does not hold, the row before the first and the one behind the last
+    (that of key V) stay as they were; two runs agree."""
+    T, D = dout.shape
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    buf = torch.randn(V + 2, D, generator=g, device="cuda")
+    start, again = buf.clone(), buf.clone()
+    d_ids = dev(ids)
+    mole.mole_embed_backward(d_ids, dout, buf[1:-1], scale)
+    mole.mole_embed_backward(d_ids, dout, again[1:-1], scale)
+    ok = (d_ids >= 0) & (d_ids < V)
+    assert mole.mole_check() == (0 if bool(ok.all()) else 5)
+    assert torch.equal(buf, again), "two runs differ"
+    rows, terms = d_ids[ok].long() + 1, dout[ok].double() * float(np.float32(scale))
+    want, mag = start.double().index_add_(0, rows, terms), start.double().abs().index_add_(0, rows, terms.abs())
+    count = torch.bincount(rows, minlength=V + 2)[:, None]
+    bound = torch.where(count > 0, (count + 4) * ref.U * mag, 0.0)
+    assert bool(((buf.double() - want).abs() <= bound).all())
+
+
+# Batches of every form of the sort (one CTA, the cluster with 1 and 4 tiles a
+# warp, through global memory) with ids outside [0, V); their key V takes one
+# digit more than the ids of V = 2^8 and 2^16.
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [72, 67])
+@pytest.mark.parametrize("V", [200, 256, 65536])
+@pytest.mark.parametrize("T", [1025, 1500, 5000, 20000, 70000])
+def test_backward_bad_ids_in_large_batches(mole, T, V, D, dtype):
+    rng = np.random.default_rng(T + V)
+    dout = _rand(rng, T, D, dtype=dtype)
+    ids = inputs.zipf_ids(rng, T, V).copy()
+    ids[rng.random(T) < 0.3] = V                     # a run of many chunks behind the last row's
+    ids[rng.random(T) < 0.05] = -1
+    ids[rng.random(T) < 0.05] = 2 ** 31 - 1
+    ids[rng.random(T) < 0.05] = V - 1                # (the run that borders on it)
+    ids[7] = -2 ** 31
+    dout[dev((ids < 0) | (ids >= V))] = float("nan")  # reaches nothing
+    _check_between_rows(mole, ids, dout, V)
+    few = inputs.zipf_ids(rng, T, V).copy()
+    few[T // 2] = V                                  # one
+    _check_between_rows(mole, few, dout.nan_to_num(), V)
+    _check_between_rows(mole, np.full(T, -7, np.int32), torch.full_like(dout, float("nan")), V)  # none left
