@@ -317,3 +317,40 @@ def test_backward_bad_ids_in_large_batches(mole, T, V, D, dtype):
     few[T // 2] = V                                  # one
     _check_between_rows(mole, few, dout.nan_to_num(), V)
     _check_between_rows(mole, np.full(T, -7, np.int32), torch.full_like(dout, float("nan")), V)  # none left
+
+
+def _runs(lengths, rng):
+    """Tokens in random order whose ids sort into runs of these lengths."""
+    return rng.permutation(np.repeat(np.arange(len(lengths)), lengths)).astype(np.int32)
+
+
+# Runs of less than a chunk, of exactly one or two and a token more or less, that
+# begin at every place of a chunk (8 tokens at these sizes).
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [64, 67])
+@pytest.mark.parametrize("length", [1, 7, 8, 9, 15, 16, 17, 23, 24, 25])
+def test_backward_runs_at_chunk_borders(mole, length, D, dtype):
+    rng = np.random.default_rng(length)
+    for offset in range(8):
+        lengths = [offset] * (offset > 0) + [length] * (2100 // length + 1)
+        ids = _runs(lengths, rng)
+        _check_between_rows(mole, ids, _rand(rng, ids.size, D, dtype=dtype), len(lengths))
+
+
+# The same with longer chunks (23 tokens at 40000 x 1024, several groups a CTA and
+# one), and with runs of all of these lengths side by side.
+@pytest.mark.parametrize("T,D,chunk", [(9000, 64, 8), (9000, 67, 8), (40000, 1024, 23), (40000, 1021, 23)])
+def test_backward_mixed_runs_at_chunk_borders(mole, T, D, chunk):
+    rng = np.random.default_rng(D)
+    for dtype in (F32, BF16):
+        near = [k * chunk + d for k in range(6) for d in (-1, 0, 1) if k * chunk + d > 0]
+        lengths = []
+        while sum(lengths) < T:
+            lengths.append(int(rng.choice(near)))
+        lengths[-1] -= sum(lengths) - T
+        assert lengths[-1] > 0
+        ids = _runs(lengths, rng)
+        assert ids.size == T
+        _check_between_rows(mole, ids, _rand(rng, T, D, dtype=dtype), len(lengths))
+        ids[ids == len(lengths) - 1] = len(lengths) + 5  # the last run: ids outside the table
+        _check_between_rows(mole, ids, _rand(rng, T, D, dtype=dtype), len(lengths) - 1)
