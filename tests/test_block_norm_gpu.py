@@ -289,3 +289,25 @@ def test_empty_batch(mole):
     dw = torch.ones(64, device="cuda")
     mole.mole_block_norm_backward(x, x, x, x, w, None, 1.0, w, dw_pre=dw, dw_post=dw.clone())
     assert mole.mole_check() == 0 and bool((dw == 1).all())
+
+
+# Rows for three turns of every CTA (as many as fit the GPU at once) in the forms
+# that the lists above give one turn: single elements of 4, 8 and 16 columns a
+# thread, over 4096 columns by units and by shifted ones, and backward rows too
+# long for the stages or for shifted units.
+@pytest.mark.parametrize("T,D,offset,tx,tf", [
+    (9400, 301, 1, BF16, F32), (7200, 1001, 1, F32, BF16), (4500, 3001, 1, BF16, BF16), (1900, 4100, 1, F32, F32),
+    (1900, 4100, 0, F32, F32), (1900, 4101, 0, BF16, F32), (1000, 5633, 0, F32, F32), (1000, 6656, 0, F32, F32),
+    (1000, 7680, 0, F32, F32), (1000, 8191, 0, F32, F32), (1000, 8192, 0, BF16, BF16), (1000, 8192, 0, F32, F32)])
+def test_many_rows(mole, T, D, offset, tx, tf):
+    rng = np.random.default_rng(D)
+    buf = torch.full((offset + (T + 1) * D,), float("nan"), dtype=tx, device="cuda")
+    x = buf[offset:offset + T * D].view(T, D)
+    x.copy_(_rand(rng, T, D, dtype=tx, std=2.0))
+    _, f, w_post, g, w_pre = _layer(rng, T, D, tx, tf)
+    _check_forward(mole, x, f, w_post, g, 0.8, w_pre, BF16)
+    _check_backward(mole, x, f, w_post, g, 0.8, w_pre, _rand(rng, T, D), _rand(rng, T, D))
+    # parts: one sum a row in place of two
+    _check_forward(mole, x, None, None, None, 1.0, w_pre, F32)
+    _check_backward(mole, x, None, None, None, 0.7, w_pre, None, _rand(rng, T, D))
+    assert bool(buf[offset + T * D:].isnan().all())
