@@ -630,7 +630,8 @@ def mole_block_norm_backward(x_out: torch.Tensor, dx_out: torch.Tensor | None, d
                              workspace: torch.Tensor | None = None, stream=None):
     """(dx, df, dgate) of mole_block_norm_forward from the gradients of its two
     outputs; dw_post and dw_pre are added to where given.  df is made where f
-    is given, dgate where gate is."""
+    is given, dgate where f and gate are; with a post-norm left out, df needs no
+    f and is written where it is passed."""
     dev = _device_of("x_out", x_out)
     if _elsewhere(stream, dev):
         with _on_stream(stream, x_out.device):
@@ -655,7 +656,7 @@ def mole_block_norm_backward(x_out: torch.Tensor, dx_out: torch.Tensor | None, d
         dx = torch.empty_like(x_out, dtype=torch.float32)
     if df is None and f is not None:
         df = torch.empty_like(x_out, dtype=torch.float32)
-    if dgate is None and gate is not None:
+    if dgate is None and gate is not None and f is not None:
         dgate = torch.empty_like(gate)
     nbytes = 0
     if workspace is not None:

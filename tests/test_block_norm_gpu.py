@@ -311,3 +311,16 @@ def test_many_rows(mole, T, D, offset, tx, tf):
     _check_forward(mole, x, None, None, None, 1.0, w_pre, F32)
     _check_backward(mole, x, None, None, None, 0.7, w_pre, None, _rand(rng, T, D))
     assert bool(buf[offset + T * D:].isnan().all())
+
+
+def test_binding_backward_gate_without_f(mole):
+    # df = gate G needs no f where there is no post-norm; dgate, which does, is not made
+    rng = np.random.default_rng(16)
+    x, _, _, g, w_pre = _layer(rng, 21, 40, F32, F32)
+    dx_out, dh = _rand(rng, 21, 40), _rand(rng, 21, 40)
+    f = _rand(rng, 21, 40)
+    want = mole.mole_block_norm_backward(x, dx_out, dh, f, None, g, 0.8, w_pre, EPS)
+    df = torch.empty_like(dx_out)
+    dx, got, dgate = mole.mole_block_norm_backward(x, dx_out, dh, None, None, g, 0.8, w_pre, EPS, df=df)
+    assert mole.mole_check() == 0 and got is df and dgate is None
+    assert torch.equal(dx, want[0]) and torch.equal(df, want[1])
