@@ -429,8 +429,9 @@ mole_status mole_embed_backward(const int32_t* ids, int64_t T, const void* dout,
  * dx [T, D], df [T, D] and dgate [T] (fp32) are overwritten; dw_pre and dw_post
  * ([D] fp32) are added to.  Any output may be NULL, not all.  dh needs w_pre;
  * x_out may be NULL where dh is; dgate, w_post and dw_post need f (dw_post
- * needs w_post too).  dx may be dx_out and df may be dh; other overlaps are
- * not allowed.  workspace (device, 16-byte aligned):
+ * needs w_post too).  dx may be dx_out, df may be dh, and dw_pre may be dw_post
+ * (both norms' weights one vector: it gets both sums); other overlaps are not
+ * allowed.  workspace (device, 16-byte aligned):
  * mole_block_norm_backward_workspace(T, D) bytes, needed for dw_pre and
  * dw_post only; calls that share one must not overlap on the GPU.
  *

@@ -735,9 +735,14 @@ extern "C" mole_status mole_block_norm_backward(const void* x_out, mole_dtype dt
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, norm_reduce_kernel, (const float*)part_pre, (const float*)part_post, ctas, (int)D,
-                           (int)part_ld(D), dw_pre, dw_post) != cudaSuccess)
-      return MOLE_ERR_CUDA;
+    auto join = [&](const float* pre, const float* post) {
+      return cudaLaunchKernelEx(&cfg, norm_reduce_kernel, pre, post, ctas, (int)D, (int)part_ld(D), dw_pre, dw_post);
+    };
+    if (dw_pre != dw_post)
+      e = join(part_pre, part_post);
+    else if ((e = join(part_pre, nullptr)) == cudaSuccess)  // one gradient for both: one sum, then the other
+      e = join(nullptr, part_post);
+    if (e != cudaSuccess) return MOLE_ERR_CUDA;
   }
   return MOLE_OK;
 }

@@ -324,3 +324,18 @@ def test_binding_backward_gate_without_f(mole):
     dx, got, dgate = mole.mole_block_norm_backward(x, dx_out, dh, None, None, g, 0.8, w_pre, EPS, df=df)
     assert mole.mole_check() == 0 and got is df and dgate is None
     assert torch.equal(dx, want[0]) and torch.equal(df, want[1])
+
+
+@pytest.mark.parametrize("T,D", [(1, 24), (45, 320), (2700, 323), (3000, 1024)])
+def test_backward_one_weight_for_both_norms(mole, T, D):
+    # w_pre is w_post and so are their gradients: both sums, dw_pre's first
+    rng = np.random.default_rng(17)
+    x, f, w, g, _ = _layer(rng, T, D, F32, F32)
+    dx_out, dh, start = _rand(rng, T, D), _rand(rng, T, D), _rand(rng, D)
+    pre, post = start.clone(), torch.zeros(D, device="cuda")
+    want = mole.mole_block_norm_backward(x, dx_out, dh, f, w, g, 0.8, w, EPS, dw_pre=pre, dw_post=post)
+    for _ in range(3):
+        dw = start.clone()
+        got = mole.mole_block_norm_backward(x, dx_out, dh, f, w, g, 0.8, w, EPS, dw_pre=dw, dw_post=dw)
+        assert mole.mole_check() == 0
+        assert torch.equal(dw, pre + post) and all(torch.equal(a, b) for a, b in zip(got, want))
