@@ -393,6 +393,8 @@ mole_status mole_train_backward(const int32_t* ids, int64_t T, const void* group
  *     workspace : device, 16-byte aligned, at least
  *       mole_embed_backward_workspace(T, D) bytes; contents unspecified on
  *       return; calls that share one must not overlap on the GPU.
+ *   More than 2048 tokens need a GPU that runs a cluster of 16 CTAs (a whole
+ *   B200 does; a partition of one may not: MOLE_ERR_CUDA, and dE as it was).
  *
  * Both take any D up to 2^20 and T up to 2^31 - 1 (T == 0 is a no-op), and
  * pointers aligned to their element; rows that start on 4 elements (D a

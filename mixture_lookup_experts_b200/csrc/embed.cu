@@ -830,9 +830,10 @@ cudaError_t launch_sums(const SumArgs& a, int n_sm, cudaStream_t stream) {
 template <int kHold>
 cudaError_t launch_sort(const SortArgs& a, cudaStream_t stream) {
   const int smem = (int)sizeof(SortSmem) + kHold * kSortThreads * (int)sizeof(int2);
-  const cudaError_t e = allow_smem(embed_sort_kernel<kHold>);
+  cudaError_t e = allow_smem(embed_sort_kernel<kHold>);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(embed_sort_kernel<kHold>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
-  cudaFuncSetAttribute(embed_sort_kernel<kHold>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   embed_sort_kernel<kHold><<<kSortCtas, kSortThreads, smem, stream>>>(a);
   return cudaGetLastError();
 }
