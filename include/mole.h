@@ -397,9 +397,9 @@ mole_status mole_train_backward(const int32_t* ids, int64_t T, const void* group
  *   B200 does; a partition of one may not: MOLE_ERR_CUDA, and dE as it was).
  *
  * Both take any D up to 2^20 and T up to 2^31 - 1 (T == 0 is a no-op), and
- * pointers aligned to their element; rows that start on 4 elements (D a
+ * pointers aligned to their element.  Rows that start on 4 elements (D a
  * multiple of 4, pointers aligned to 16 bytes, bf16 ones to 8) take the vector
- * kernels.
+ * kernels, and so does the lookup in a bf16 table of any D with such pointers.
  */
 mole_status mole_embed_forward(const int32_t* ids, int64_t T, const void* E, int64_t V, int64_t D, float scale,
                                mole_dtype dt_E, void* out, mole_dtype dt_out, cudaStream_t stream);
@@ -439,9 +439,9 @@ mole_status mole_embed_backward(const int32_t* ids, int64_t T, const void* dout,
  *
  * Both take any D up to 8192 and T up to 2^31 - 1 (T == 0 is a no-op), and
  * pointers aligned to their element; where all pointers to rows and weights are
- * aligned to 16 bytes (bf16 ones to 8) the rows take vector accesses, of any D
- * as long as two of them fit shared memory (fp32 backward: up to 5632 columns
- * where D is not a multiple of 4).
+ * aligned to 16 bytes (bf16 ones to 8) the rows take vector accesses.  Where D
+ * is not a multiple of 4 that goes up to D = 8189 in the forward pass, and in the
+ * backward up to 5629 (x_out and f fp32), 6141 (one of them) or 6653 (bf16).
  */
 mole_status mole_block_norm_forward(const void* x, mole_dtype dt_x, const void* f, mole_dtype dt_f,
                                     const float* w_post, const float* gate, float res_scale, const float* w_pre,
@@ -477,8 +477,9 @@ mole_status mole_block_norm_backward(const void* x_out, mole_dtype dt_x, const v
  *
  * The step number and the rate come from the host struct, or, where step_dev
  * or lr_dev is not NULL, from device memory when the kernel runs (a captured
- * step then follows them on every replay); grad_scale_dev (NULL = 1) is a
- * factor on every gradient, such as a clipping factor computed on the device.
+ * step then follows them on every replay; a device step below 1 is not noticed
+ * and makes the weights NaN); grad_scale_dev (NULL = 1) is a factor on every
+ * gradient, such as a clipping factor computed on the device.
  *
  * tensors and config are HOST structs, read before the call returns.  No
  * memory that a call writes may overlap anything else in its list

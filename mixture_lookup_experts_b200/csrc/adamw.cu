@@ -169,7 +169,7 @@ struct Factors {
 // The thread's units of a chunk whose first element it has is e0.  kFull: the
 // whole chunk lies in the tensor, with vector accesses; its types are template
 // parameters then (tests per unit made the 8-bit kernel issue-bound: 89
-// instructions an element, 67 now; 619 -> 527 us for 185 M elements).
+// instructions an element, 67 now).
 template <bool kState8, bool kFull, bool kGradBf16, bool kParamBf16, bool kMaster>
 __device__ __forceinline__ void step_chunk(const AdamArgs& a, const AdamTensor& t, const Factors& w, int64_t e0) {
   using G = std::conditional_t<kGradBf16, uint16_t, float>;
@@ -284,9 +284,12 @@ __device__ __forceinline__ void step_types(const AdamArgs& a, const AdamTensor& 
   }
 }
 
-// CTAs per SM (the registers that a thread gets): 185 M elements under load with
-// 8-bit states 576 us at 4, 557 at 5, 699 at 6 (spills); fp32 states 824 us at 4,
-// 815 at 3, 835 at 5.  (Two elements an instruction, fp32x2, is slower: 640 us.)
+// CTAs per SM (the registers that a thread gets): 185 M elements, one step on an
+// idle GPU and (in brackets) steps without a pause, at the clocks that the power
+// limit leaves.  8-bit states: 524 us (582) at 4 (64 registers), 510 (561) at 5
+// (48, 120 bytes of spill stores), 612 (695) at 6 (40, 624 bytes); two elements an
+// instruction (fp32x2) is slower, (640).  fp32 states: 813 us (815) at 3, 821
+// (822) at 4, 836 (840) at 5.
 template <bool kState8>
 __global__ void __launch_bounds__(kAdamThreads, kState8 ? 5 : 3) adamw_kernel(const __grid_constant__ AdamArgs a) {
   __shared__ float factors[3];

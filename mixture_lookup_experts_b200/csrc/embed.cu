@@ -753,9 +753,10 @@ __global__ void __launch_bounds__(kSortThreads, 1)
 
 // Tokens per chunk: enough (chunk, slice) groups to fill the GPU several times
 // over (888 to 2368 groups measured within 5 % of each other at 16384 x 2048 and
-// 65536 x 1024), no more than 256, so that the partial sums (2 rows of D per
-// chunk) stay small beside the rows of dout, and no more than leave room for the
-// CTA's groups' tokens in 64 KB of shared memory (narrow rows: up to 128 groups).
+// 65536 x 1024).  At least 8, so that the partial sums (2 fp32 rows of D per chunk)
+// take no more workspace than T D bytes (half of a bf16 dout).  At most 256, since
+// one group works through a chunk alone, and no more than leave room for the CTA's
+// groups' tokens in 64 KB of shared memory (narrow rows: up to 128 groups).
 int chunk_tokens(int64_t T, int64_t D) {
   const RowSplit r = row_split(D, 4 * kChunkUnits, kChunkThreads);
   const int64_t groups = std::max<int64_t>(1, kChunkGroups * (kChunkThreads / r.tx) / r.slices);

@@ -615,7 +615,7 @@ template <Form kForm, class X, class F>
 cudaError_t backward_units(const NormBwd& a, int n_sm, int* ctas, cudaStream_t stream) {
   const RowPlan p = row_plan(kForm, false, a.T, a.D);
   if (p.threads > kRowThreads) {
-    if constexpr (kForm == kUnits)  // (of more than 7040 columns, two fp32 rows do not fit shared memory)
+    if constexpr (kForm == kUnits)  // (two rows of over 6656 columns, fp32, do not fit shared memory)
       if (stage_bytes(kForm, kStages, p, 8 + sizeof(X) + sizeof(F)) > kMaxSmem)
         return backward_launch<kForm, false, 16, 0, kMaxRowThreads, X, F>(a, p, n_sm, ctas, stream);
     return backward_launch<kForm, false, 16, kStages, kMaxRowThreads, X, F>(a, p, n_sm, ctas, stream);

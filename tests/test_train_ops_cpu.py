@@ -249,3 +249,12 @@ def test_adamw_eps_range(mole):
                         (1e300, 1), (float("inf"), 1)):
         t, cfg = _adam(mole, 1, eps=eps)
         assert mole.lib.mole_adamw_step(t, 1, ctypes.addressof(cfg), None) == status, eps
+
+
+def test_embed_workspace_of_the_shortest_chunks(mole):
+    # chunks of 8 tokens: two fp32 rows of partial sums each, T D bytes in all
+    for T, D in ((2100, 64), (9000, 67), (14000, 1024)):
+        size = mole.mole_embed_backward_workspace(T, D)
+        chunks = (T + 7) // 8
+        least = 2 * 8 * T + 16 + 8 * chunks + 2 * 4 * D * chunks
+        assert least <= size <= least + 4 * 255, (T, D)
