@@ -493,7 +493,12 @@ def _on_stream(stream, dev: torch.device):
             yield
             return
         if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+            handle = int(stream)
+            if handle == 2:  # cudaStreamPerThread: torch allocates nothing for it
+                raise ValueError("the per-thread default stream is not supported, pass a stream")
+            # 0 and cudaStreamLegacy (ExternalStream takes 0 for "any stream of the pool")
+            stream = (torch.cuda.default_stream(dev) if handle in (0, 1)
+                      else torch.cuda.ExternalStream(handle, device=dev))
         if stream.device != dev:
             raise ValueError(f"stream of {stream.device}, tensors on {dev}")
         with torch.cuda.stream(stream):

@@ -180,3 +180,46 @@ def test_norm_backward_before_kernels_that_start_early(mole):
         torch.cuda.synchronize()
         assert torch.equal(got, want)
     assert mole.mole_check() == 0
+
+
+def test_streams_by_handle(mole):
+    """A stream given by its handle (0: the default stream, as the other calls
+    take it) gets the kernels behind what it holds already; so does a torch
+    stream."""
+    T, V, D = 3000, 400, 256
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    ids = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    E, X, F, C, w = rnd(V, D), rnd(T, D), rnd(T, D), rnd(T, D), rnd(D)
+
+    def run(stream):
+        dE, dw, p, m, v = (torch.zeros(s, device="cuda") for s in ((V, D), (D,), (V, D), (V, D), (V, D)))
+        x = torch.zeros_like(X)
+        torch.cuda._sleep(20_000_000)  # (some 10 ms: what follows is not there before)
+        x.copy_(X)
+        out = mole.mole_embed_forward(ids, E, 2.0, stream=stream)
+        x1, h = mole.mole_block_norm_forward(x, F, w, None, 0.5, w, stream=stream)
+        dx, df, _ = mole.mole_block_norm_backward(x1, C, C, F, w, None, 0.5, w, dw_pre=dw, stream=stream)
+        mole.mole_embed_backward(ids, dx, dE, stream=stream)
+        mole.mole_adamw_step([p], [dE], [m], [v], stream=stream)
+        return [t.clone() for t in (out, x1, h, dx, df, dw, dE, p)]
+
+    dev0 = E.device
+    for handle in (0, 1, torch.cuda.default_stream().cuda_stream):
+        with mole._on_stream(handle, dev0):
+            assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    with pytest.raises(ValueError, match="per-thread"):
+        run(2)
+    want = run(None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for current, stream in ((torch.cuda.default_stream(), 0), (torch.cuda.default_stream(), 1), (side, side),
+                            (side, side.cuda_stream)):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(current):
+            got = run(stream)
+        torch.cuda.synchronize()
+        assert mole.mole_check() == 0
+        for a, b in zip(want, got):
+            assert torch.equal(a, b), stream
