@@ -339,3 +339,27 @@ def test_backward_one_weight_for_both_norms(mole, T, D):
         got = mole.mole_block_norm_backward(x, dx_out, dh, f, w, g, 0.8, w, EPS, dw_pre=dw, dw_post=dw)
         assert mole.mole_check() == 0
         assert torch.equal(dw, pre + post) and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("T,D", [(1048600, 2056), (2200000, 981)])
+def test_rows_beyond_2_31_elements(mole, T, D):
+    # the last rows and some at 2^31 elements: the bits of a call on them alone
+    rng = np.random.default_rng(D)
+    part = 3000                                          # (rows that take the same kernels)
+    at = [0, (1 << 31) // D // 4 * 4 - 2000, T // 4 * 4 - part]  # (rows and their shifts)
+    x, f, w_post, g, w_pre = _layer(rng, part, D, BF16, BF16)
+    dx_out, dh = _rand(rng, part, D), _rand(rng, part, D)
+    want = (*mole.mole_block_norm_forward(x, f, w_post, g, 0.8, w_pre, EPS),
+            *mole.mole_block_norm_backward(x, dx_out, dh, f, w_post, g, 0.8, w_pre, EPS))
+    big = [torch.zeros(T, *t.shape[1:], dtype=t.dtype, device="cuda") for t in (x, f, g, dx_out, dh)]
+    for i in at:
+        for b, t in zip(big, (x, f, g, dx_out, dh)):
+            b[i:i + part] = t
+    X, F, G, DX, DH = big
+    backward = mole.mole_block_norm_backward(X, DX, DH, F, w_post, G, 0.8, w_pre, EPS, dx=DX, df=DH)
+    forward = mole.mole_block_norm_forward(X, F, w_post, G, 0.8, w_pre, EPS, x_out=X)
+    assert mole.mole_check() == 0
+    for got, w in zip((*forward, *backward), want):
+        for i in at:
+            assert torch.equal(got[i:i + part], w), i
+        assert not got[part:at[1]].any() and not got[at[1] + part:at[2]].any()

@@ -354,3 +354,34 @@ def test_backward_mixed_runs_at_chunk_borders(mole, T, D, chunk):
         _check_between_rows(mole, ids, _rand(rng, T, D, dtype=dtype), len(lengths))
         ids[ids == len(lengths) - 1] = len(lengths) + 5  # the last run: ids outside the table
         _check_between_rows(mole, ids, _rand(rng, T, D, dtype=dtype), len(lengths) - 1)
+
+
+def test_backward_beyond_2_31_elements(mole):
+    # a gradient of 2^31 + elements: the same bits as with the rows put together
+    rng = np.random.default_rng(9)
+    T, V, D = 3000, 1048600, 2056
+    few = np.sort(rng.choice(V, 300, replace=False))
+    few[0], few[-1] = 0, V - 1
+    small = rng.integers(0, 300, T).astype(np.int32)
+    small[:2] = 0, 299
+    dout = _rand(rng, T, D)
+    want = mole.mole_embed_backward(dev(small), dout, torch.ones(300, D, device="cuda"), 1.5)
+    dE = torch.ones(V, D, device="cuda")
+    mole.mole_embed_backward(dev(few[small].astype(np.int32)), dout, dE, 1.5)
+    assert mole.mole_check() == 0
+    rows = dev(few)
+    assert torch.equal(dE[rows], want)
+    dE[rows] = 1.0
+    assert float(dE.min()) == 1.0 and float(dE.max()) == 1.0
+    del dE, want, dout
+    # rows of dout behind 2^31 elements: the last tokens are all that is not zero
+    T, V, D, last = 1048600, 50, 2056, 64
+    dout = torch.zeros(T, D, dtype=BF16, device="cuda")
+    dout[-last:] = _rand(rng, last, D, dtype=BF16)
+    ids = torch.randint(0, V, (T,), dtype=torch.int32, device="cuda")
+    dE = torch.zeros(V, D, device="cuda")
+    mole.mole_embed_backward(ids, dout, dE)
+    assert mole.mole_check() == 0
+    # (adding zeros rounds nothing)
+    want, bound = ref.embed_backward(ids[-last:].cpu().numpy(), ref.f64(dout[-last:]), np.zeros((V, D)), 1.0, V)
+    ref.assert_within(ref.f64(dE), want, bound)
