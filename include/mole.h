@@ -416,8 +416,9 @@ mole_status mole_embed_backward(const int32_t* ids, int64_t T, const void* dout,
  * so one call takes a block's output f (mole_ffn_block without its residual,
  * mole_lookup_combine, ...) to the next stream x' and the next block's input;
  * with f NULL it is the norm before the first block, with h NULL the end of
- * the last one.  All arithmetic in fp32; h is computed from x' before x' is
- * rounded to dt_x.
+ * the last one.  All arithmetic in fp32 (the sum of a row's squares too: rows
+ * whose sum passes 2^128, of values around 10^18, are not served); h is computed
+ * from x' before x' is rounded to dt_x.
  *   x : [T, D] dt_x   f : [T, D] dt_f or NULL   w_post, w_pre : [D] fp32 or NULL
  *   gate : [T] fp32 or NULL   x_out : [T, D] dt_x or NULL (may be x)
  *   h : [T, D] dt_h or NULL (needs w_pre; not overlapping any other tensor)
