@@ -223,3 +223,38 @@ def test_streams_by_handle(mole):
         assert mole.mole_check() == 0
         for a, b in zip(want, got):
             assert torch.equal(a, b), stream
+
+
+def test_capture_with_the_streams_handle(mole):
+    """Calls captured with the capturing stream's handle, workspaces made in the
+    capture: a replay gives the results of the calls one by one."""
+    T, V, D = 3000, 400, 256
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    ids = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    E, X, F, C, w = rnd(V, D), rnd(T, D), rnd(T, D), rnd(T, D), rnd(D)
+
+    def run(sums, stream):
+        dE, dw, p, m, v = sums
+        out = mole.mole_embed_forward(ids, E, 2.0, stream=stream)
+        x1, h = mole.mole_block_norm_forward(X, F, w, None, 0.5, w, stream=stream)
+        dx, df, _ = mole.mole_block_norm_backward(x1, C, C, F, w, None, 0.5, w, dw_pre=dw, stream=stream)
+        mole.mole_embed_backward(ids, dx, dE, stream=stream)
+        mole.mole_adamw_step([p], [dE], [m], [v], stream=stream)
+        return out, x1, h, dx, df
+
+    make = lambda: [torch.zeros(s, device="cuda") for s in ((V, D), (D,), (V, D), (V, D), (V, D))]  # noqa: E731
+    sums, once = make(), make()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(sums, torch.cuda.current_stream().cuda_stream)
+    want = run(once, None)
+    for _ in range(2):
+        for t in sums:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((*want, *once), (*got, *sums)):
+            assert torch.equal(a, b)
+    assert mole.mole_check() == 0
